@@ -1,0 +1,237 @@
+"""Cases, inputs and plain forms of the operators around the W8A8 linear layer.
+
+Three operators of one decode or prefill step:
+
+* norm: residual addition, root-mean-square norm and 8-bit output, as e4m3
+  codes with a scale per 128 columns (the input of the block-FP8 product) or
+  as int8 codes with a scale per token (the input of the int8 product);
+* gemm: the matrix product in 8-bit integers with a scale per token and per
+  weight row, bf16 out;
+* verify: acceptance of drafted tokens against the target's probabilities
+  from given random numbers, and the draw of the token that follows them.
+
+`run` computes them in elementary torch operations, or with `own` set
+through this repository's package. All are inference operators: there is no
+backward pass.
+"""
+
+import torch
+
+own = False
+
+E4M3_MAX = 448.0
+I8_MAX = 127.0
+GROUP = 128
+EPS = 1e-6
+# device memory that a serving program keeps for the calls that take scratch
+WORKSPACE_BYTES = 64 << 20
+
+
+def listed():
+    return [
+        # one token's hidden state before a linear layer: latency
+        {"name": "norm_e4m3_decode", "op": "norm", "out": "e4m3", "m": 1, "k": 5120, "residual": True},
+        # seven drafts and the current token of one stream
+        {"name": "norm_i8_verify", "op": "norm", "out": "i8", "m": 8, "k": 5120, "residual": True},
+        # a 3,465-token prompt
+        {"name": "norm_e4m3_prefill", "op": "norm", "out": "e4m3", "m": 3465, "k": 5120, "residual": True},
+        # an odd batch of prompt tokens, a wide row, no residual stream
+        {"name": "norm_i8_wide", "op": "norm", "out": "i8", "m": 2049, "k": 8704, "residual": False},
+        # one token's merged query, key and value projection
+        {"name": "gemm_decode", "op": "gemm", "m": 1, "n": 7168, "k": 5120},
+        # four drafts and the current token through the widest projection
+        {"name": "gemm_verify", "op": "gemm", "m": 5, "n": 17408, "k": 5120},
+        # a batch of concurrent streams through the deepest projection
+        {"name": "gemm_batch", "op": "gemm", "m": 63, "n": 5120, "k": 8704},
+        # a short prompt, one token past a whole tile
+        {"name": "gemm_prompt", "op": "gemm", "m": 257, "n": 8192, "k": 5120},
+        # a 3,465-token prompt through the widest projection
+        {"name": "gemm_prefill", "op": "gemm", "m": 3465, "n": 17408, "k": 5120},
+        # one stream with three drafts
+        {"name": "verify_one", "op": "verify", "b": 1, "drafts": 3, "v": 152064, "type": "fp32", "q": True},
+        # many streams, drafts that are certain (a lookup in the prompt), probabilities kept in bf16, odd vocabulary
+        {"name": "verify_lookup", "op": "verify", "b": 33, "drafts": 4, "v": 151937, "type": "bf16", "q": False},
+        # many streams with seven drafts each
+        {"name": "verify_batch", "op": "verify", "b": 64, "drafts": 7, "v": 152064, "type": "fp32", "q": True},
+    ]
+
+
+def _spread(rng, low, high):
+    """A whole number of low..high, spread evenly over its logarithm."""
+    return min(high, max(low, int(round(low * (high / low) ** rng.random()))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "gemm", "verify"])
+    if op == "norm":
+        return {"op": op, "out": rng.choice(["e4m3", "i8"]), "m": _spread(rng, 1, 3465), "k": GROUP * rng.randint(4, 68),
+                "residual": rng.random() < 0.7}
+    if op == "gemm":
+        return {"op": op, "m": _spread(rng, 1, 3465), "n": _spread(rng, 512, 17408), "k": GROUP * rng.randint(4, 40)}
+    return {"op": op, "b": _spread(rng, 1, 64), "drafts": rng.randint(1, 7), "v": _spread(rng, 4000, 152064),
+            "type": rng.choice(["fp32", "bf16"]), "q": rng.random() < 0.7}
+
+
+def _generator(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _activation(rows, cols, g):
+    """Hidden states: Gaussian, one entry in a thousand 20 times larger."""
+    x = torch.randn(rows, cols, device="cuda", generator=g)
+    return torch.where(torch.rand(rows, cols, device="cuda", generator=g) < 0.001, 20.0 * x, x)
+
+
+def _int8_rows(x):
+    """int8 codes and the scale of each row of a fp32 matrix."""
+    s = x.abs().amax(1, keepdim=True) / I8_MAX
+    return (x / s).round().clamp(-I8_MAX, I8_MAX).to(torch.int8), s[:, 0].contiguous()
+
+
+def prepare(case, seed):
+    g = _generator(seed)
+    if case["op"] == "norm":
+        m, k = case["m"], case["k"]
+        return {
+            "op": "norm", "out": case["out"],
+            "x": _activation(m, k, g).to(torch.bfloat16),
+            "residual": (3.0 * _activation(m, k, g)).to(torch.bfloat16) if case["residual"] else None,
+            "weight": (1.0 + 0.1 * torch.randn(k, device="cuda", generator=g)).to(torch.bfloat16),
+        }
+    workspace = torch.empty(WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    if case["op"] == "gemm":
+        m, n, k = case["m"], case["n"], case["k"]
+        a_q, a_s = _int8_rows(_activation(m, k, g))
+        w_q, w_s = _int8_rows(0.02 * torch.randn(n, k, device="cuda", generator=g))
+        return {"op": "gemm", "a_q": a_q, "a_s": a_s, "w_q": w_q, "w_s": w_s, "workspace": workspace}
+    b, drafts, v = case["b"], case["drafts"], case["v"]
+    kind = torch.float32 if case["type"] == "fp32" else torch.bfloat16
+    logits = 2.5 * torch.randn(b, drafts + 1, v, device="cuda", generator=g)
+    # a drafter that follows the target: its logits are the target's and some noise
+    near = logits[:, :drafts] + 0.6 * torch.randn(b, drafts, v, device="cuda", generator=g)
+    target = torch.softmax(logits, -1).to(kind)
+    draft = torch.softmax(near, -1)
+    race = -torch.log(1.0 - torch.rand(b, drafts, v, device="cuda", generator=g))
+    tokens = (draft / race).argmax(-1).to(torch.int32)  # one draw of each draft distribution
+    return {
+        "op": "verify", "target": target, "draft": draft.to(kind) if case["q"] else None, "tokens": tokens,
+        "u_accept": torch.rand(b, drafts, device="cuda", generator=g),
+        "u_sample": torch.rand(b, device="cuda", generator=g), "workspace": workspace,
+    }
+
+
+def _norm(s):
+    x, r = s["x"], s["residual"]
+    h = x if r is None else (x.float() + r.float()).to(torch.bfloat16)
+    # the mean square and its root in 64 bits: a last bit here would move values across the codes' rounding borders
+    inv = (1.0 / (h.double().square().mean(1, keepdim=True) + EPS).sqrt()).float()
+    y = ((h.float() * inv) * s["weight"].float()).to(torch.bfloat16).float()
+    m, k = y.shape
+    top = torch.tensor(E4M3_MAX if s["out"] == "e4m3" else I8_MAX, device=y.device)
+    groups = y.view(m, k // GROUP, GROUP) if s["out"] == "e4m3" else y.view(m, 1, k)
+    amax = groups.abs().amax(2, keepdim=True)
+    scale = torch.where(amax > 0, amax / top, torch.ones_like(amax))
+    q = torch.minimum(torch.maximum(groups / scale, -top), top)
+    if s["out"] == "e4m3":
+        return q.view(m, k).to(torch.float8_e4m3fn), scale[:, :, 0], h
+    return q.round().view(m, k).to(torch.int8), scale[:, 0, 0], h
+
+
+def _gemm(s):
+    sums = s["a_q"].float() @ s["w_q"].float().t()
+    return (sums * (s["a_s"][:, None] * s["w_s"])).to(torch.bfloat16)
+
+
+def _verify(s):
+    target, draft, tokens = s["target"], s["draft"], s["tokens"].long()
+    b, drafts = tokens.shape
+    v = target.shape[2]
+    at = tokens[:, :, None]
+    p = target[:, :drafts].gather(2, at)[:, :, 0].double()
+    q = torch.ones_like(p) if draft is None else draft.gather(2, at)[:, :, 0].double()
+    accepted = (s["u_accept"].double() * q < p).long().cumprod(1).sum(1)  # drafts before the first rejection
+    rows = torch.arange(b, device=target.device)
+    rest = target[rows, accepted].float()
+    last = accepted.clamp(max=drafts - 1)
+    rejected = (accepted < drafts)[:, None]
+    if draft is None:
+        away = torch.zeros_like(rest).scatter_(1, tokens[rows, last][:, None], 1.0)
+    else:
+        away = draft[rows, last].float()
+    left = torch.where(rejected, rest - away, rest)
+
+    def whole(w):  # weights in units of 2^-32
+        return (w * 4294967296.0).round().double().nan_to_num(0.0).clamp(0.0, 4294967295.0).long()
+
+    weights = whole(left)
+    weights = torch.where(weights.sum(1, keepdim=True) > 0, weights, whole(rest))
+    cum = weights.cumsum(1)
+    total = cum[:, -1]
+    point = (s["u_sample"].double() * 4294967296.0).long()
+    # floor(total * point / 2^32) in 64 bits
+    low = (total & 0xFFFFFFFF) * (point >> 16) + (((total & 0xFFFFFFFF) * (point & 0xFFFF)) >> 16)
+    goal = (total >> 32) * point + (low >> 16)
+    drawn = (cum <= goal[:, None]).sum(1)
+    drawn = torch.where(total > 0, drawn, torch.full_like(drawn, -1))
+    place = torch.arange(drafts + 1, device=target.device)[None]
+    kept = torch.cat([tokens, tokens[:, :1]], 1)
+    out = torch.where(place < accepted[:, None], kept, torch.full_like(kept, -1))
+    out = torch.where(place == accepted[:, None], drawn[:, None], out)
+    return out.to(torch.int32), accepted.to(torch.int32)
+
+
+def _own(s):
+    import memory_bound_w8a8_amd as fp8bq
+
+    if s["op"] == "norm":
+        if s["out"] == "e4m3":
+            codes, scales, h = fp8bq.rmsnorm_quant(s["x"], s["weight"], s["residual"], EPS)
+            return codes.view(torch.float8_e4m3fn), scales, h
+        return fp8bq.rmsnorm_quant_i8(s["x"], s["weight"], s["residual"], EPS)
+    if s["op"] == "gemm":
+        return fp8bq.gemm_i8(s["a_q"], s["a_s"], s["w_q"], s["w_s"], workspace=s["workspace"])
+    return fp8bq.verify_drafts(s["target"], s["tokens"], s["u_accept"], s["u_sample"], draft_p=s["draft"],
+                               workspace=s["workspace"])
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"norm": _norm, "gemm": _gemm, "verify": _verify}[state["op"]](state)
+
+
+def work(case):
+    if case["op"] == "norm":
+        m, k = case["m"], case["k"]
+        scales = m * (k // GROUP if case["out"] == "e4m3" else 1)
+        return {"bytes": m * k * (7 if case["residual"] else 3) + 2 * k + 4 * scales, "flops": 10 * m * k}
+    if case["op"] == "gemm":
+        m, n, k = case["m"], case["n"], case["k"]
+        return {"bytes": n * k + m * k + 2 * m * n + 4 * (m + n), "flops": 2 * m * n * k}
+    # one row of probabilities of each stream has to be read whole, and the drafter's beside it where it has one
+    b, drafts, v = case["b"], case["drafts"], case["v"]
+    each = 4 if case["type"] == "fp32" else 2
+    rows = 2 if case["q"] else 1
+    small = b * drafts * (4 + 4 + each * rows) + 4 * b + 4 * b * (drafts + 2)
+    return {"bytes": b * v * each * rows + small, "flops": 4 * b * v}
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "verify":
+        return None  # tokens and counts: whole numbers
+    if case["op"] == "gemm":
+        wide = torch.matmul(s["a_q"].to(torch.float64), s["w_q"].to(torch.float64).t())  # exact: below 2^53
+        return wide * torch.outer(s["a_s"].to(torch.float64), s["w_s"].to(torch.float64))
+    h = s["x"].to(torch.float64)
+    if s["residual"] is not None:
+        h = h + s["residual"].to(torch.float64)
+    kept = h.to(torch.bfloat16).to(torch.float64)  # the residual stream is bf16
+    norm = kept / torch.linalg.vector_norm(kept, dim=1, keepdim=True).square().div(case["k"]).add(EPS).sqrt()
+    # the norm's output is bf16, as the quantisation's input is everywhere
+    y = (norm * s["weight"].to(torch.float64)).to(torch.bfloat16).to(torch.float64)
+    if case["out"] == "e4m3":
+        groups = y.reshape(-1, GROUP)
+        scale = groups.abs().max(1).values / E4M3_MAX
+        return (groups / scale[:, None]).reshape(y.shape), scale.reshape(case["m"], -1), h
+    return None, y.abs().max(1).values / I8_MAX, h
