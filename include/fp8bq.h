@@ -52,8 +52,9 @@ typedef enum fp8bq_status {
     FP8BQ_ERR_ALIGN = -3,  /* code/bf16 pointer not 16-B aligned, fp32 not 4-B */
     FP8BQ_ERR_DEVICE = -4, /* no HIP device, or the current device is not gfx950 */
     FP8BQ_ERR_LAUNCH = -5, /* the HIP runtime rejected a kernel launch        */
-    FP8BQ_ERR_SCRATCH = -6 /* the request needs more than the library's static
+    FP8BQ_ERR_SCRATCH = -6, /* the request needs more than the library's static
                               scratch buffer (fp8bq_topk_bf16_noalloc)       */
+    FP8BQ_ERR_VALUE = -7   /* a scalar argument is outside its range         */
 } fp8bq_status;
 
 /*

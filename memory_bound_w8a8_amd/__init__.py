@@ -457,3 +457,8 @@ def mb_mfma_scaled(grid: int, iters: int, codes: torch.Tensor, scale: float, sin
            lib().fp8bq_mb_mfma_e4m3_scaled(int(grid), int(iters), _ptr(codes), float(scale), _ptr(sink),
                                            torch.cuda.current_stream(codes.device).cuda_stream))
     return sink
+
+
+# The operators around the linear layer (include/fp8bq_step.h).
+from .step import (STEP_EXPORTS, gemm_i8, gemm_i8_workspace_bytes, quant_act_i8, quant_weight_i8,  # noqa: E402
+                   rmsnorm_quant, rmsnorm_quant_i8, verify_drafts, verify_workspace_bytes)

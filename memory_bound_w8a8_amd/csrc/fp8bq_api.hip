@@ -2,50 +2,27 @@
 // of every entry point is documented in include/fp8bq.h.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
-#include <cstring>
-
+#include "api_checks.h"
 #include "fp8bq.h"
 #include "launch.h"
 
 namespace {
 
-constexpr int64_t kMaxElems = int64_t(1) << 40;  // bound on M*K, N*K, M*N
+using fp8bq::aligned;
+using fp8bq::check_device;
+using fp8bq::launch_status;
+using fp8bq::product_ok;
+
 constexpr int64_t kStreamMaxM = 64;              // streaming kernels: 1..64 tokens per launch on any shape
 constexpr int64_t kStreamSplitMaxM = 128;        // forced streaming path up to 128 tokens (two launches past 64
                                                  // where the 65..80 instances do not serve)
 constexpr int64_t kTiledMaxK = int64_t(1) << 24; // tiled kernel: 32-bit offsets within a 256-row tile
-constexpr int kMaxDevices = 64;
 constexpr int64_t kSmallMaxM = 16;               // weight-only path: one 16-token tile
 constexpr int64_t kFusedMaxM = 8;                // fused path: quantisation layouts for up to 8 tokens
 constexpr int64_t kSmallMaxK = 72 * 128;         // groups within their instance tables
 constexpr int64_t kTopkMaxK = 256;               // survivors per row
 constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;  // vocabulary indices are int32
 constexpr int64_t kMaxGridBlocks = int64_t(1) << 21;   // 1024-thread workgroups in one 1-D grid
-
-// Per-device capability cache: 0 = unknown, 1 = gfx950, -1 = not usable.
-std::atomic<int> g_device_ok[kMaxDevices];
-
-int check_device() {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return FP8BQ_ERR_DEVICE;
-  if (dev >= kMaxDevices) return FP8BQ_ERR_DEVICE;
-  int state = g_device_ok[dev].load(std::memory_order_acquire);
-  if (state == 0) {
-    hipDeviceProp_t prop;
-    state = -1;
-    if (hipGetDeviceProperties(&prop, dev) == hipSuccess && std::strncmp(prop.gcnArchName, "gfx950", 6) == 0)
-      state = 1;
-    g_device_ok[dev].store(state, std::memory_order_release);
-  }
-  return state == 1 ? FP8BQ_OK : FP8BQ_ERR_DEVICE;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool product_ok(int64_t a, int64_t b) { return a == 0 || b <= kMaxElems / a; }
-
-int launch_status(hipError_t e) { return e == hipSuccess ? FP8BQ_OK : FP8BQ_ERR_LAUNCH; }
 
 int check_gemm_args(int64_t M, int64_t N, int64_t K, const void* A_fp8, const float* A_scales, const void* W_fp8,
                     const float* W_scales, void* C_bf16) {
@@ -327,6 +304,7 @@ const char* fp8bq_status_string(int status) {
     case FP8BQ_ERR_ALIGN: return "misaligned pointer (codes/bf16 need 16 B, fp32 scales 4 B)";
     case FP8BQ_ERR_DEVICE: return "no usable HIP device (gfx950 required)";
     case FP8BQ_ERR_LAUNCH: return "kernel launch failed";
+    case FP8BQ_ERR_VALUE: return "an argument's value is outside its range";
     case FP8BQ_ERR_SCRATCH: return "request needs more than the library's static scratch buffer (4 MiB per GPU)";
     default: return "unknown status";
   }

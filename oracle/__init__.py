@@ -31,6 +31,9 @@ Modules:
 * ``scoring`` -- two-stage vocabulary scoring: exact top-k of coarse logits
   and exact fp64 rescoring of the survivors (page 1's FP8-screen,
   BF16-score scheme).
+* ``step`` -- the operators around the linear layer: norm with the residual's
+  addition, int8 quantisation by rows, the int8 product, verification of
+  drafted tokens.
 
 Every function is pinned by ``-m "not gpu"`` tests against something other
 than itself (torch's float8_e4m3fn casts, exact rational brute force, closed
@@ -42,6 +45,7 @@ from .quant import quant_act_ref, quant_weight_ref
 from .gemm import gemm_ref, gemm_ref_at
 from .w8a16 import gemm_w8a16_ref, gemm_w8a16_ref_at
 from .scoring import bf16_key, rescore_ref, topk_ref
+from .step import draw_ref, gemm_i8_ref, quant_rows_i8_ref, rmsnorm_ref, verify_ref, weight_units
 
 __all__ = [
     "E4M3_MAX",
@@ -57,4 +61,10 @@ __all__ = [
     "bf16_key",
     "topk_ref",
     "rescore_ref",
+    "rmsnorm_ref",
+    "quant_rows_i8_ref",
+    "gemm_i8_ref",
+    "weight_units",
+    "draw_ref",
+    "verify_ref",
 ]
