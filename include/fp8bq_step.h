@@ -30,8 +30,8 @@ extern "C" {
  * Residual addition, root-mean-square norm and 8-bit output in one launch.
  *
  *   h   = bf16(x + r)                      (h = x without a residual)
- *   inv = fp32(1 / sqrt(mean_k(h^2) + eps)) (mean and root in 64 bits)
- *   y   = bf16((h * inv) * weight)         (fp32 products)
+ *   inv = 1 / sqrt(mean_k(h^2) + eps)      (64 bits)
+ *   y   = bf16(fp32((h * inv) * weight))   (products in 64 bits)
  *   fp8bq_rmsnorm_quant:    codes, scales = fp8bq_quant_act(y)
  *   fp8bq_rmsnorm_quant_i8: codes, scales = fp8bq_quant_act_i8(y)
  *
@@ -42,9 +42,9 @@ extern "C" {
  *           residual (it may be R_bf16 or X_bf16 itself: each element is
  *           read before it is written), NULL or ignored without one.
  *   codes, scales: written, as fp8bq_quant_act / fp8bq_quant_act_i8 write
- *           them, which give the same bits for the same y. The mean square is
- *           summed in 64 bits from exact squares, so the codes do not depend
- *           on the order of the sum.
+ *           them, which give the same bits for the same y. With 64 bits up
+ *           to the rounding of y, the order of the sum shows in no code but
+ *           where a value lies within some 2^-50 of a rounding border.
  * M == 0 or K == 0 is a quick return. NaN or infinite inputs give unspecified
  * codes in their row. Errors: NULL pointer; M < 0, K < 0, K % 128 != 0,
  * K > FP8BQ_NORM_MAX_K, M >= 2^31 or M*K > 2^40; eps not finite or <= 0

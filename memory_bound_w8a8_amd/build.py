@@ -29,9 +29,6 @@ HIPCC_FLAGS = [
     "-Wall",
     # keep the compiler from forming packed-fp32 VALU ops
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # MFMA results in ordinary VGPRs: the per-group scale FMAs read them
-    # directly instead of copying each out of an accumulation register
-    "-mllvm", "-amdgpu-mfma-vgpr-form=true",
     # unroll the chunk loops in full even where in-kernel quantisation makes
     # them long: a partly rolled loop indexes the register arrays at run time,
     # which puts them in scratch memory
@@ -39,6 +36,11 @@ HIPCC_FLAGS = [
     f"-I{INCLUDE}",
     f"-I{CSRC}",
 ]
+# MFMA results in ordinary VGPRs: the per-group scale FMAs read them directly
+# instead of copying each out of an accumulation register. Not for the int8
+# product, whose sums stay in the accumulation registers (256 per wave).
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]
+ACC_FORM_SOURCES = {"gemm_i8.hip"}
 
 
 def _hipcc() -> str:
@@ -62,7 +64,8 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(f for f in os.listdir(CSRC) if f.endswith(".hip"))
     objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in sources]
-    cmds = [[hipcc, *HIPCC_FLAGS, "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(sources, objs)]
+    form = lambda s: [] if s in ACC_FORM_SOURCES else VGPR_FORM  # noqa: E731
+    cmds = [[hipcc, *HIPCC_FLAGS, *form(s), "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(sources, objs)]
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(cmds))) as ex:
         for out in ex.map(_run, cmds):
             if verbose and out.strip():

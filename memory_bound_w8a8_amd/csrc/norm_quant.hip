@@ -3,7 +3,10 @@
 //
 // Page 3 (zskr.cn blog), section 3.3, fuses the norm with the quantisation of
 // the linear layer's input; section 2.2 stores weights as INT8. Per row:
-//   h = bf16(x + r), inv = fp32(1 / sqrt(mean(h^2) + eps)), y = bf16((h inv) w),
+//   h = bf16(x + r), inv = 1 / sqrt(mean(h^2) + eps), y = bf16((h inv) w),
+// the sum of squares, the root and the two products in 64 bits: an fp32
+// product rounds a few values in 10^8 to the other side of a bf16 border,
+// which moves the scale of their group by 2^-8 where they are its maximum.
 // then y is quantised as fp8bq_quant_act does (a scale per 128 columns) or to
 // int8 with a scale per row. Rounding y to bf16 is what the separate norm and
 // quantiser do (their interface is bf16), so the fused codes equal theirs bit
@@ -97,7 +100,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, c
       for (int j = 0; j < 8; ++j) sum = fma(static_cast<double>(f[j]), static_cast<double>(f[j]), sum);
     }
     sum = block_sum(sum, sums);
-    const float inv = static_cast<float>(1.0 / sqrt(sum / k + eps));
+    const double inv = 1.0 / sqrt(sum / k + eps);
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -108,7 +111,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, c
       unpack8(h[c], f);
       unpack8(wv, g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[c][j] = pack_bf16x2((f[2 * j] * inv) * g[2 * j], (f[2 * j + 1] * inv) * g[2 * j + 1]);
+      for (int j = 0; j < 4; ++j)
+        h[c][j] = pack_bf16x2(static_cast<float>((f[2 * j] * inv) * g[2 * j]),
+                              static_cast<float>((f[2 * j + 1] * inv) * g[2 * j + 1]));
       unpack8(h[c], f);
       float amax = 0.f;
 #pragma unroll

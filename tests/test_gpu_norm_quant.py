@@ -1,11 +1,12 @@
 """GPU: norm with the residual's addition and 8-bit output, and the int8
 quantisers, bitwise against the oracle.
 
-Codes, scales and residual have to be equal bit for bit: the mean square is
-summed in 64 bits on both sides, so inv = fp32(1 / sqrt(mean + eps)) can
-differ only where the 64-bit value lies within about 2^-50 of a border
-between two fp32 numbers (one row in 10^7 or fewer), and every later
-operation is a single correctly rounded one on both sides."""
+Codes, scales and residual have to be equal bit for bit: the norm is computed
+in 64 bits on both sides up to the rounding of y, so y can differ only where
+its 64-bit value lies within about 2^-50 of a rounding border (one value in
+10^8 or fewer, 2^-50 against the borders' distance of 2^-24 before the second
+rounding), and every later operation is a single correctly rounded one on both
+sides."""
 
 import numpy as np
 import pytest
