@@ -33,7 +33,7 @@ hipError_t launch_gemm_i8(int64_t m, int64_t n, int64_t k, const void* aq, const
                           const float* ws, void* c, void*, hipStream_t stream) {
   if (m > 512) return tile<256, 256, 2, 2, 2>(m, n, k, aq, as, wq, ws, c, stream);
   if (m > 64) return tile<128, 128, 2, 2, 4>(m, n, k, aq, as, wq, ws, c, stream);
-  return tile<64, 64, 2, 2, 6>(m, n, k, aq, as, wq, ws, c, stream);
+  return launch_gemm_i8_rows(m, n, k, aq, as, wq, ws, c, stream);
 }
 
 }  // namespace fp8bq

@@ -74,6 +74,13 @@ __device__ __forceinline__ void buffer_dma16(const v4i& buf, unsigned voff, unsi
                : "memory", "m0");
 }
 
+// The same for data that is read once.
+__device__ __forceinline__ void buffer_dma16_once(const v4i& buf, unsigned voff, unsigned soff, unsigned lds_base) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds" ::"v"(voff), "s"(buf),
+               "s"(soff), "s"(__builtin_amdgcn_readfirstlane(static_cast<int>(lds_base)))
+               : "memory", "m0");
+}
+
 template <int BM, int BN, int WM, int WN, int STAGES>
 struct I8Tile {
   static constexpr int kWaves = WM * WN;

@@ -22,6 +22,10 @@ int64_t gemm_i8_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_gemm_i8(int64_t m, int64_t n, int64_t k, const void* aq, const float* as, const void* wq,
                           const float* ws, void* c, void* workspace, hipStream_t stream);
 
+// gemm_i8_rows.hip: m <= 64
+hipError_t launch_gemm_i8_rows(int64_t m, int64_t n, int64_t k, const void* aq, const float* as, const void* wq,
+                               const float* ws, void* c, hipStream_t stream);
+
 // verify.hip
 int64_t verify_workspace_bytes(int64_t b, int64_t v);
 hipError_t launch_verify(int64_t b, int n_drafts, int64_t v, bool bf16, const void* target, const void* draft,
