@@ -8,11 +8,17 @@
 // 16 TILES), its 8 waves split K. A wave walks its groups of 128 columns; per
 // group first the 16-token blocks of the activation, then the 16-row tiles of
 // its weights, each a chunk of 16 rows x 128 bytes. Chunks are copied to the
-// wave's own ring of 8 slots in LDS, without registers and without barriers:
-// chunk c + 7 goes out while chunk c is used, 112 KB in flight per CU. A copy
-// instruction reads 8 whole 128-byte lines; rows past the range lie past the
-// buffer's end and read nothing. In a slot, piece c of row r stands at
-// c ^ (r & 7), which spreads the fragment reads over the banks.
+// wave's own ring of 4 slots in LDS, without registers and without barriers:
+// chunk c + 3 goes out before chunk c is used, 48 KB in flight per CU. More
+// slots bring nothing while a launch's start grows by 0.1 us for each 16 KB of
+// LDS (7168 x 5120 at 1 token: 7.8 / 8.0 / 8.2 / 8.4 / 8.5 us with 3 / 4 / 6 /
+// 8 / 10 slots; 17408 x 5120 at 64: 22.8 / 22.5 / 22.3 / 22.0 / 22.5), and two
+// workgroups per CU of half the rows are slower (16.6 -> 17.4 us at 17408 x
+// 5120, 5 tokens: twice the activation). A copy instruction reads 8 whole
+// 128-byte lines, the weights' marked as read once (16.9 against 18.1 us
+// without the mark); rows past the range lie past the buffer's end and read
+// nothing. In a slot, piece c of row r stands at c ^ (r & 7), which spreads the
+// fragment reads over the banks.
 //
 // The sums are 32-bit integers, exact in any order; the 8 waves' sums are
 // added through LDS, scaled, rounded to bf16 and stored.
@@ -25,7 +31,7 @@ namespace fp8bq {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kSlots = 8;          // ring slots per wave
+constexpr int kSlots = 4;          // ring slots per wave
 constexpr int kSlotBytes = 2048;   // 16 rows x 128 bytes
 constexpr int kMaxRowTiles = 5;    // 16-row tiles per workgroup
 constexpr int64_t kCUs = 256;
@@ -151,9 +157,9 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_i8_rows_kernel(int m_rows, i
       }
     __syncthreads();
 #pragma unroll
-    for (int y = first / kWaves; y < MINE && y < (first + ROUND) / kWaves; ++y) {
+    for (int y = 0; y < MINE; ++y) {
       const int item = wave + kWaves * y;
-      if (item >= ITEMS) continue;
+      if (item < first || item >= first + ROUND || item >= ITEMS) continue;
       v4i sum = v4i{0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w)
