@@ -8,12 +8,14 @@
 // is bound by that read, 4 or 8 bytes per word and sequence.
 //
 // The draw works on whole numbers (weights in units of 2^-32, 64-bit sums),
-// so splitting a row over workgroups and threads cannot change the token.
-//   1. verify_sums_kernel: a row is cut into `splits` pieces, one workgroup
-//      each; every workgroup finds its sequence's rejection by itself and
-//      writes its piece's sum.
-//   2. verify_draw_kernel: one workgroup per sequence finds the piece that
-//      holds the drawn point and scans it.
+// so cutting a row into parts cannot change the token.
+//   1. verify_sums_kernel: each wave of a row's workgroups sums one part of
+//      it, 16 bytes a lane and load. Every wave finds its sequence's rejection
+//      by itself (two dependent loads); the first one writes it down.
+//   2. verify_draw_kernel: one workgroup of 16 waves per sequence finds the
+//      part that holds the drawn point by a scan over the parts' sums, one a
+//      thread, and scans that part the same way. A part is short enough for
+//      one trip of the workgroup up to 4,000,000 words.
 #include "device_common.h"
 #include "step_launch.h"
 
@@ -23,8 +25,11 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kSumThreads = 256;
+constexpr int kSumWaves = kSumThreads / 64;
+constexpr int kDrawThreads = 1024;
+constexpr int kDrawWaves = kDrawThreads / 64;
+constexpr int kMaxParts = kDrawThreads;  // the scan over the parts: one a thread
 
 struct Verify {
   int n_drafts;
@@ -35,13 +40,40 @@ struct Verify {
   const int* draft_len;  // null: n_drafts each
   const float* u_accept;
   const float* u_sample;
+  // workspace: a sum of each part of each sequence's row, and what became of
+  // the sequence's drafts (accepted ones, + kRejected where one was rejected)
+  u64* sums;
+  int* state;
+  int parts;
+  int64_t part_words;
 };
+constexpr int kRejected = 256;
 
 template <bool BF16>
 __device__ __forceinline__ float prob(const void* p, int64_t i) {
   if constexpr (BF16) return bf16_lo(static_cast<const unsigned short*>(p)[i]);
   return static_cast<const float*>(p)[i];
 }
+
+// 16 bytes of probabilities from any word: a row of an odd vocabulary starts
+// at a multiple of the word's size only.
+template <bool BF16>
+struct Vec {
+  static constexpr int kWords = BF16 ? 8 : 4;
+  typedef v4u __attribute__((aligned(2))) at2;
+  typedef v4u __attribute__((aligned(4))) at4;
+  v4u raw;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (BF16)
+      raw = *reinterpret_cast<const at2*>(static_cast<const unsigned short*>(p) + i);
+    else
+      raw = *reinterpret_cast<const at4*>(static_cast<const float*>(p) + i);
+  }
+  __device__ __forceinline__ float word(int j) const {
+    if constexpr (BF16) return j & 1 ? bf16_hi(raw[j >> 1]) : bf16_lo(raw[j >> 1]);
+    return __builtin_bit_cast(float, static_cast<unsigned>(raw[j]));
+  }
+};
 
 // Nearest whole number of 2^-32 (ties to even). The hardware conversion
 // holds results to 0 .. 2^32 - 1 and gives 0 for NaN.
@@ -81,8 +113,8 @@ __device__ __forceinline__ int accepted_drafts(const Verify& a, int64_t b, bool*
 template <bool BF16>
 struct Row {
   const void* p;
-  const void* q;      // null: nothing, or 1 at `certain`
-  int64_t certain;    // -1: none
+  const void* q;    // null: nothing, or 1 at `certain`
+  int64_t certain;  // -1: none
   __device__ __forceinline__ Row(const Verify& a, int64_t b, int r, bool less) {
     const int each = BF16 ? 2 : 4;
     p = static_cast<const char*>(a.target) + (b * (a.n_drafts + 1) + r) * a.v * each;
@@ -103,57 +135,123 @@ __device__ __forceinline__ u64 wave_sum(u64 v) {
   return v;
 }
 
-__device__ __forceinline__ u64 block_sum(u64 v, u64* slots) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
-  __syncthreads();
-  u64 s = 0;
-  for (int i = 0; i < kWaves; ++i) s += slots[i];
-  __syncthreads();
-  return s;
+// This lane's share of the weights of [lo, hi), without the certain draft's 1:
+// vectors lane, lane + lanes, ... of the range; LESS: p - q.
+template <bool BF16, bool LESS>
+__device__ __forceinline__ u64 sum_words(const Row<BF16>& row, int64_t lo, int64_t hi, int lane, int lanes) {
+  using V = Vec<BF16>;
+  constexpr int W = V::kWords, U = 4;  // U vectors of each tensor in flight
+  u64 sum = 0;
+  const int64_t step = static_cast<int64_t>(lanes) * W;
+  int64_t i = lo + static_cast<int64_t>(lane) * W;
+  for (; i + (U - 1) * step + W <= hi; i += U * step) {
+    V p[U], q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      p[u].load(row.p, i + u * step);
+      if constexpr (LESS) q[u].load(row.q, i + u * step);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < W; ++j) sum += weight_units(LESS ? p[u].word(j) - q[u].word(j) : p[u].word(j));
+  }
+  for (; i < hi; i += step) {
+    if (i + W <= hi) {
+      V p, q;
+      p.load(row.p, i);
+      if constexpr (LESS) q.load(row.q, i);
+#pragma unroll
+      for (int j = 0; j < W; ++j) sum += weight_units(LESS ? p.word(j) - q.word(j) : p.word(j));
+    } else {
+      for (int64_t x = i; x < hi; ++x)
+        sum += weight_units(LESS ? prob<BF16>(row.p, x) - prob<BF16>(row.q, x) : prob<BF16>(row.p, x));
+    }
+  }
+  return sum;
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void verify_sums_kernel(Verify a, u64* __restrict__ part) {
-  __shared__ u64 slots[kWaves];
+__global__ __launch_bounds__(kSumThreads) void verify_sums_kernel(Verify a) {
   const int64_t b = blockIdx.y;
+  const int lane = threadIdx.x & 63;
+  const int part = blockIdx.x * kSumWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   bool rejected;
   const int r = accepted_drafts<BF16>(a, b, &rejected);
+  if (part == 0 && lane == 0) a.state[b] = r + (rejected ? kRejected : 0);
+  if (part >= a.parts) return;
   const Row<BF16> row(a, b, r, rejected);
-  const int64_t piece = (a.v + gridDim.x - 1) / gridDim.x;
-  const int64_t lo = piece * blockIdx.x;
-  const int64_t hi = lo + piece < a.v ? lo + piece : a.v;
-  u64 sum = 0;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) sum += row.at(i);
-  sum = block_sum(sum, slots);
-  if (threadIdx.x == 0) part[b * gridDim.x + blockIdx.x] = sum;
+  const int64_t lo = a.part_words * part;
+  const int64_t hi = lo + a.part_words < a.v ? lo + a.part_words : a.v;
+  u64 sum = row.q != nullptr ? sum_words<BF16, true>(row, lo, hi, lane, 64) : sum_words<BF16, false>(row, lo, hi, lane, 64);
+  sum = wave_sum(sum);
+  if (lane == 0) {
+    if (row.certain >= lo && row.certain < hi)
+      sum += static_cast<u64>(row.at(row.certain)) - weight_units(prob<BF16>(row.p, row.certain));
+    a.sums[b * a.parts + part] = sum;
+  }
+}
+
+// Inclusive sums over the workgroup's threads in order; *total: all of them.
+// A barrier on both sides lets `slots` be used again.
+__device__ __forceinline__ u64 block_scan(u64 w, u64* slots, u64* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const u64 up = __shfl_up(w, off, 64);
+    if (lane >= off) w += up;
+  }
+  if (lane == 63) slots[wave] = w;
+  __syncthreads();
+  u64 base = 0, all = 0;
+#pragma unroll
+  for (int j = 0; j < kDrawWaves; ++j) {
+    const u64 s = slots[j];
+    if (j < wave) base += s;
+    all += s;
+  }
+  __syncthreads();
+  *total = all;
+  return base + w;
 }
 
 // The lowest index of [lo, hi) whose running sum (starting from `sum`) exceeds
 // `goal`, or -1; the same in every thread.
 template <bool BF16>
 __device__ int64_t scan_row(const Row<BF16>& row, int64_t lo, int64_t hi, u64 sum, u64 goal, u64* slots, int* found) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  using V = Vec<BF16>;
+  constexpr int W = V::kWords;
   if (threadIdx.x == 0) *found = -1;
   __syncthreads();
-  for (int64_t at = lo; at < hi; at += kThreads) {
-    const int64_t i = at + threadIdx.x;
-    const u64 w = i < hi ? row.at(i) : 0;
-    u64 run = w;
+  for (int64_t at = lo; at < hi; at += kDrawThreads * W) {
+    const int64_t i = at + threadIdx.x * W;
+    unsigned w[W];
+    if (i + W <= hi) {
+      V p, q;
+      p.load(row.p, i);
+      if (row.q != nullptr) q.load(row.q, i);
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const u64 up = __shfl_up(run, off, 64);
-      if (lane >= off) run += up;
+      for (int j = 0; j < W; ++j) {
+        float x = p.word(j);
+        if (row.q != nullptr) x -= q.word(j);
+        if (i + j == row.certain) x -= 1.f;
+        w[j] = weight_units(x);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j] = i + j < hi ? row.at(i + j) : 0;
     }
-    if (lane == 63) slots[wave] = run;
-    __syncthreads();
-    u64 base = sum;
-    for (int j = 0; j < kWaves; ++j) {
-      if (j < wave) base += slots[j];
-      sum += slots[j];
+    u64 mine = 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) mine += w[j];
+    u64 trip;
+    u64 run = sum + block_scan(mine, slots, &trip) - mine;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      if (run <= goal && run + w[j] > goal) *found = threadIdx.x * W + j;  // one word at most: sums rise
+      run += w[j];
     }
-    run += base;
-    if (run > goal && run - w <= goal) *found = threadIdx.x;  // one thread at most: sums rise
+    sum += trip;
     __syncthreads();
     if (*found >= 0) return at + *found;
   }
@@ -161,68 +259,76 @@ __device__ int64_t scan_row(const Row<BF16>& row, int64_t lo, int64_t hi, u64 su
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void verify_draw_kernel(Verify a, const u64* __restrict__ part, int splits,
-                                                               int* __restrict__ tokens, int* __restrict__ accepted) {
-  __shared__ u64 slots[kWaves];
+__global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(Verify a, int* __restrict__ tokens,
+                                                                   int* __restrict__ accepted) {
+  __shared__ u64 slots[kDrawWaves];
   __shared__ int found;
+  __shared__ int at_part;
+  __shared__ u64 before_part;
   const int64_t b = blockIdx.x;
-  bool rejected;
-  const int r = accepted_drafts<BF16>(a, b, &rejected);
-  float s = a.u_sample[b] * 0x1p32f;
+  const int t = threadIdx.x;
+  const int state = a.state[b];
+  const u64 part = t < a.parts ? a.sums[b * a.parts + t] : 0;
+  const int kept = t < a.n_drafts ? a.drafts[b * a.n_drafts + t] : -1;
+  const float s = a.u_sample[b] * 0x1p32f;
   unsigned s32;
   asm("v_cvt_u32_f32 %0, %1" : "=v"(s32) : "v"(s));
   const u64 point = static_cast<u64>(s32) << 32;
+  const bool rejected = (state & kRejected) != 0;
+  const int r = state & (kRejected - 1);
 
-  u64 total = 0;
-  for (int i = 0; i < splits; ++i) total += part[b * splits + i];
+  u64 total;
+  const u64 run = block_scan(part, slots, &total);
   int64_t token = -1;
   if (total > 0) {
     const u64 goal = __umul64hi(total, point);  // floor(total * z / 2^32) < total
-    const int64_t piece = (a.v + splits - 1) / splits;
-    u64 before = 0;
-    int at = 0;
-    while (at + 1 < splits && before + part[b * splits + at] <= goal) before += part[b * splits + at++];
-    const int64_t lo = piece * at;
-    const int64_t hi = lo + piece < a.v ? lo + piece : a.v;
-    token = scan_row<BF16>(Row<BF16>(a, b, r, rejected), lo, hi, before, goal, slots, &found);
+    if (run > goal && run - part <= goal) {     // one part: sums rise
+      at_part = t;
+      before_part = run - part;
+    }
+    __syncthreads();
+    const int64_t lo = a.part_words * at_part;
+    const int64_t hi = lo + a.part_words < a.v ? lo + a.part_words : a.v;
+    token = scan_row<BF16>(Row<BF16>(a, b, r, rejected), lo, hi, before_part, goal, slots, &found);
   } else if (rejected) {  // the drafter's row covers the target's: the target's itself
     const Row<BF16> row(a, b, r, false);
-    u64 sum = 0;
-    for (int64_t i = threadIdx.x; i < a.v; i += kThreads) sum += row.at(i);
-    sum = block_sum(sum, slots);
+    u64 sum;
+    block_scan(sum_words<BF16, false>(row, 0, a.v, t, kDrawThreads), slots, &sum);
     if (sum > 0) token = scan_row<BF16>(row, 0, a.v, 0, __umul64hi(sum, point), slots, &found);
   }
-  for (int i = threadIdx.x; i <= a.n_drafts; i += kThreads)
-    tokens[b * (a.n_drafts + 1) + i] =
-        i < r ? a.drafts[b * a.n_drafts + i] : (i == r ? static_cast<int>(token) : -1);
-  if (threadIdx.x == 0) accepted[b] = r;
+  if (t <= a.n_drafts) tokens[b * (a.n_drafts + 1) + t] = t < r ? kept : (t == r ? static_cast<int>(token) : -1);
+  if (t == 0) accepted[b] = r;
 }
 
-int split_count(int64_t b, int64_t v) {
-  int64_t s = (1024 + b - 1) / b;
-  const int64_t most = (v + 1023) / 1024;  // at least 1024 words per piece
-  s = s < most ? s : most;
-  return static_cast<int>(s < 256 ? s : 256);
+// Parts of a row: some 8192 waves in all (32 on each CU), at least 256 words
+// a wave (one load a lane), and as many as the second kernel has threads.
+int part_count(int64_t b, int64_t v) {
+  const int64_t fill = (8192 + b - 1) / b, most = (v + 255) / 256;
+  const int64_t s = fill < most ? fill : most;
+  return static_cast<int>(s < kMaxParts ? s : kMaxParts);
 }
 
 }  // namespace
 
-int64_t verify_workspace_bytes(int64_t b, int64_t v) { return b == 0 ? 0 : 8 * b * split_count(b, v); }
+int64_t verify_workspace_bytes(int64_t b, int64_t v) { return b * (8 * part_count(b == 0 ? 1 : b, v) + 4); }
 
 hipError_t launch_verify(int64_t b, int n_drafts, int64_t v, bool bf16, const void* target, const void* draft,
                          const int* drafts, const int* draft_len, const float* u_accept, const float* u_sample,
                          void* workspace, int* tokens, int* accepted, hipStream_t stream) {
-  const Verify a{n_drafts, v, target, draft, drafts, draft_len, u_accept, u_sample};
-  const int splits = split_count(b, v);
-  u64* part = static_cast<u64*>(workspace);
-  const dim3 grid(static_cast<unsigned>(splits), static_cast<unsigned>(b));
+  const int parts = part_count(b, v);
+  u64* sums = static_cast<u64*>(workspace);
+  // whole 16-byte vectors a part, so that only the row's own start can be off
+  const int64_t part_words = ((v + parts - 1) / parts + 7) / 8 * 8;
+  const Verify a{n_drafts, v,    target, draft,  drafts, draft_len, u_accept, u_sample, sums,
+                 reinterpret_cast<int*>(sums + b * parts), parts, part_words};
+  const dim3 grid(static_cast<unsigned>((parts + kSumWaves - 1) / kSumWaves), static_cast<unsigned>(b));
   const dim3 seqs(static_cast<unsigned>(b));
   if (bf16) {
-    hipLaunchKernelGGL(verify_sums_kernel<true>, grid, dim3(kThreads), 0, stream, a, part);
-    hipLaunchKernelGGL(verify_draw_kernel<true>, seqs, dim3(kThreads), 0, stream, a, part, splits, tokens, accepted);
+    hipLaunchKernelGGL(verify_sums_kernel<true>, grid, dim3(kSumThreads), 0, stream, a);
+    hipLaunchKernelGGL(verify_draw_kernel<true>, seqs, dim3(kDrawThreads), 0, stream, a, tokens, accepted);
   } else {
-    hipLaunchKernelGGL(verify_sums_kernel<false>, grid, dim3(kThreads), 0, stream, a, part);
-    hipLaunchKernelGGL(verify_draw_kernel<false>, seqs, dim3(kThreads), 0, stream, a, part, splits, tokens, accepted);
+    hipLaunchKernelGGL(verify_sums_kernel<false>, grid, dim3(kSumThreads), 0, stream, a);
+    hipLaunchKernelGGL(verify_draw_kernel<false>, seqs, dim3(kDrawThreads), 0, stream, a, tokens, accepted);
   }
   return hipGetLastError();
 }
