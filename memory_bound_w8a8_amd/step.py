@@ -59,57 +59,67 @@ def step_lib():
     return _calls
 
 
-def _enqueue(name, device, *args):
-    """The call with `device` current and its current stream as last argument."""
-    fn = getattr(step_lib(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+# At a single token the kernels take 3 to 8 us, about as long as a call's way
+# through Python, so that way is kept short: one check per tensor (0.3 us),
+# outputs from empty_like where a tensor of their shape is at hand (1.2 us
+# against 1.7), the raw handle of the current stream (0.1 us; its Stream object
+# takes 2.7).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_empty, _empty_like = torch.empty, torch.empty_like
+_BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
+
+
+def _enqueue(name, index, *args):
+    """The call with GPU `index` current and its current stream as last argument."""
+    fn = getattr(_calls or step_lib(), name)
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream)
-    _check(name, st)
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st != 0:
+        _check(name, st)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: on {t.device}, expected {device}")
+def _on(t, name, dtype, ndim, index):
+    """_need(), and that t is on GPU `index`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.get_device() == index
+            and t.is_contiguous()):
+        return
+    _need(t, name, dtype, ndim)
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _rmsnorm(name, x, weight, residual, eps, out_residual, scale_cols, code_dtype):
-    _need(x, "x", torch.bfloat16, 2)
-    _need(weight, "weight", torch.bfloat16, 1)
+def _rmsnorm(name, x, weight, residual, eps, out_residual, code_dtype):
+    _need(x, "x", _BF16, 2)
+    at = x.get_device()
+    _on(weight, "weight", _BF16, 1, at)
     m, k = x.shape
     if weight.shape[0] != k:
         raise ValueError(f"weight has {weight.shape[0]} entries, x has {k} columns")
-    h = None
+    h = x
     if residual is not None:
-        _need(residual, "residual", torch.bfloat16, 2)
+        _on(residual, "residual", _BF16, 2, at)
         if residual.shape != x.shape:
             raise ValueError(f"residual is {tuple(residual.shape)}, x is {tuple(x.shape)}")
         if out_residual is None:
-            h = torch.empty_like(x)
+            h = _empty_like(x)
         else:
-            _need(out_residual, "out_residual", torch.bfloat16, 2)
+            _on(out_residual, "out_residual", _BF16, 2, at)
             if out_residual.shape != x.shape:
                 raise ValueError(f"out_residual is {tuple(out_residual.shape)}, x is {tuple(x.shape)}")
             h = out_residual
     elif out_residual is not None:
         raise ValueError("out_residual needs a residual")
-    _same_device(x.device, weight=weight, residual=residual, out_residual=h)
-    codes = torch.empty((m, k), dtype=code_dtype, device=x.device)
-    scales = torch.empty((m, scale_cols(k)) if scale_cols else (m,), dtype=torch.float32, device=x.device)
-    _enqueue(name, x.device, m, k, _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(h), _ptr(codes),
-             _ptr(scales))
-    return codes, scales, x if h is None else h
-
-
-def _groups(k):
-    return k // 128 if k % 128 == 0 else 0
+    codes = _empty_like(x, dtype=code_dtype)
+    scales = _empty((m, k // 128) if code_dtype is _U8 else (m,), dtype=_F32, device=x.device)
+    if residual is None:
+        _enqueue(name, at, m, k, x.data_ptr(), None, weight.data_ptr(), float(eps), None, codes.data_ptr(),
+                 scales.data_ptr())
+    else:
+        _enqueue(name, at, m, k, x.data_ptr(), residual.data_ptr(), weight.data_ptr(), float(eps), h.data_ptr(),
+                 codes.data_ptr(), scales.data_ptr())
+    return codes, scales, h
 
 
 def rmsnorm_quant(x, weight, residual=None, eps=1e-6, out_residual=None):
@@ -117,20 +127,20 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, out_residual=None):
     returns (uint8 e4m3fn codes [M, K] and fp32 scales [M, K/128] of y,
     bitwise quant_act(y), and h). out_residual: where h is written
     (`residual` itself, for an update in place); allocated when None."""
-    return _rmsnorm("fp8bq_rmsnorm_quant", x, weight, residual, eps, out_residual, _groups, torch.uint8)
+    return _rmsnorm("fp8bq_rmsnorm_quant", x, weight, residual, eps, out_residual, _U8)
 
 
 def rmsnorm_quant_i8(x, weight, residual=None, eps=1e-6, out_residual=None):
     """rmsnorm_quant() with int8 codes [M, K] and one fp32 scale per row [M],
     bitwise quant_act_i8(y)."""
-    return _rmsnorm("fp8bq_rmsnorm_quant_i8", x, weight, residual, eps, out_residual, None, torch.int8)
+    return _rmsnorm("fp8bq_rmsnorm_quant_i8", x, weight, residual, eps, out_residual, _I8)
 
 
 def _quant_rows(name, x):
     rows, k = x.shape
-    codes = torch.empty((rows, k), dtype=torch.int8, device=x.device)
-    scales = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    _enqueue(name, x.device, rows, k, _ptr(x), _ptr(codes), _ptr(scales))
+    codes = _empty_like(x, dtype=_I8)
+    scales = _empty((rows,), dtype=_F32, device=x.device)
+    _enqueue(name, x.get_device(), rows, k, x.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -154,13 +164,16 @@ def gemm_i8_workspace_bytes(m, n, k):
     return st
 
 
-def _scratch(workspace, need, device):
-    """A caller's uint8 workspace, or one allocated here; None where none is needed."""
+def _scratch(workspace, need, index):
+    """(address, bytes) of a caller's uint8 workspace, or of one allocated
+    here (None: `need` is 0), and the tensor that holds it."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
-    _need(workspace, "workspace", torch.uint8, 1)
-    _same_device(device, workspace=workspace)
-    return workspace
+        if need == 0:
+            return None, 0, None
+        workspace = _empty((need,), dtype=_U8, device=index)
+    else:
+        _on(workspace, "workspace", _U8, 1, index)
+    return workspace.data_ptr(), workspace.shape[0], workspace
 
 
 def gemm_i8(a_q, a_s, w_q, w_s, out=None, workspace=None):
@@ -168,27 +181,26 @@ def gemm_i8(a_q, a_s, w_q, w_s, out=None, workspace=None):
     codes [M, K] and [N, K], fp32 scales [M] and [N], bf16 [M, N]. workspace
     (uint8, on the device): allocated when None and of use; one that is too
     small is not used. The result does not depend on it."""
-    _need(a_q, "a_q", torch.int8, 2)
-    _need(w_q, "w_q", torch.int8, 2)
-    _need(a_s, "a_s", torch.float32, 1)
-    _need(w_s, "w_s", torch.float32, 1)
+    _need(a_q, "a_q", _I8, 2)
+    at = a_q.get_device()
+    _on(w_q, "w_q", _I8, 2, at)
+    _on(a_s, "a_s", _F32, 1, at)
+    _on(w_s, "w_s", _F32, 1, at)
     m, k = a_q.shape
     n, k2 = w_q.shape
     if k != k2:
         raise ValueError(f"K mismatch: a_q has {k}, w_q has {k2}")
     if a_s.shape[0] != m or w_s.shape[0] != n:
         raise ValueError(f"scale shapes {tuple(a_s.shape)}, {tuple(w_s.shape)} do not match M={m}, N={n}")
-    device = a_q.device
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=device)
+        out = _empty((m, n), dtype=_BF16, device=a_q.device)
     else:
-        _need(out, "out", torch.bfloat16, 2)
+        _on(out, "out", _BF16, 2, at)
         if tuple(out.shape) != (m, n):
             raise ValueError(f"out must be [{m}, {n}]")
-    _same_device(device, w_q=w_q, a_s=a_s, w_s=w_s, out=out)
-    workspace = _scratch(workspace, gemm_i8_workspace_bytes(m, n, k) if workspace is None else 0, device)
-    _enqueue("fp8bq_gemm_i8", device, m, n, k, _ptr(a_q), _ptr(a_s), _ptr(w_q), _ptr(w_s), _ptr(out),
-             _ptr(workspace), 0 if workspace is None else workspace.numel())
+    scratch, nbytes, _keep = _scratch(workspace, gemm_i8_workspace_bytes(m, n, k) if workspace is None else 0, at)
+    _enqueue("fp8bq_gemm_i8", at, m, n, k, a_q.data_ptr(), a_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(),
+             out.data_ptr(), scratch, nbytes)
     return out
 
 
@@ -209,35 +221,35 @@ def verify_drafts(target_p, drafts, u_accept, u_sample, draft_p=None, draft_len=
     drafts], u_sample fp32 [B], draft_len int32 [B] (None: all). Returns
     (tokens int32 [B, drafts + 1]: the accepted drafts, the drawn token, then
     -1; accepted int32 [B])."""
-    if not isinstance(target_p, torch.Tensor) or target_p.dtype not in (torch.float32, torch.bfloat16):
+    if not isinstance(target_p, torch.Tensor) or target_p.dtype not in (_F32, _BF16):
         raise TypeError("target_p: expected a float32 or bfloat16 torch.Tensor")
-    _need(target_p, "target_p", target_p.dtype, 3)
-    _need(drafts, "drafts", torch.int32, 2)
-    _need(u_accept, "u_accept", torch.float32, 2)
-    _need(u_sample, "u_sample", torch.float32, 1)
+    kind = target_p.dtype
+    _need(target_p, "target_p", kind, 3)
+    at = target_p.get_device()
+    _on(drafts, "drafts", _I32, 2, at)
+    _on(u_accept, "u_accept", _F32, 2, at)
+    _on(u_sample, "u_sample", _F32, 1, at)
     b, k = drafts.shape
-    v = target_p.shape[2]
-    if tuple(target_p.shape[:2]) != (b, k + 1):
+    rows, places, v = target_p.shape
+    if rows != b or places != k + 1:
         raise ValueError(f"target_p must be [{b}, {k + 1}, V], got {tuple(target_p.shape)}")
-    if tuple(u_accept.shape) != (b, k) or u_sample.shape[0] != b:
+    if u_accept.shape != drafts.shape or u_sample.shape[0] != b:
         raise ValueError(f"u_accept must be [{b}, {k}] and u_sample [{b}]")
+    q = lens = None
     if draft_p is not None:
-        _need(draft_p, "draft_p", target_p.dtype, 3)
+        _on(draft_p, "draft_p", kind, 3, at)
         if tuple(draft_p.shape) != (b, k, v):
             raise ValueError(f"draft_p must be [{b}, {k}, {v}], got {tuple(draft_p.shape)}")
-        if k == 0:
-            draft_p = None
+        q = draft_p.data_ptr() if k > 0 else None
     if draft_len is not None:
-        _need(draft_len, "draft_len", torch.int32, 1)
+        _on(draft_len, "draft_len", _I32, 1, at)
         if draft_len.shape[0] != b:
             raise ValueError(f"draft_len must be [{b}]")
-    device = target_p.device
-    _same_device(device, drafts=drafts, u_accept=u_accept, u_sample=u_sample, draft_p=draft_p, draft_len=draft_len)
-    need = verify_workspace_bytes(b, k, v)
-    workspace = _scratch(workspace, need, device)
-    tokens = torch.empty((b, k + 1), dtype=torch.int32, device=device)
-    accepted = torch.empty((b,), dtype=torch.int32, device=device)
-    _enqueue("fp8bq_verify_drafts", device, b, k, v, F32 if target_p.dtype == torch.float32 else BF16, _ptr(target_p),
-             _ptr(draft_p), _ptr(drafts), _ptr(draft_len), _ptr(u_accept), _ptr(u_sample), _ptr(workspace),
-             0 if workspace is None else workspace.numel(), _ptr(tokens), _ptr(accepted))
+        lens = draft_len.data_ptr()
+    scratch, nbytes, _keep = _scratch(workspace, verify_workspace_bytes(b, k, v) if workspace is None else 0, at)
+    tokens = _empty((b, k + 1), dtype=_I32, device=target_p.device)
+    accepted = _empty_like(u_sample, dtype=_I32)
+    _enqueue("fp8bq_verify_drafts", at, b, k, v, F32 if kind is _F32 else BF16, target_p.data_ptr(), q,
+             drafts.data_ptr(), lens, u_accept.data_ptr(), u_sample.data_ptr(), scratch, nbytes, tokens.data_ptr(),
+             accepted.data_ptr())
     return tokens, accepted
