@@ -31,7 +31,7 @@ extern "C" {
  *
  *   h   = bf16(x + r)                      (h = x without a residual)
  *   inv = 1 / sqrt(mean_k(h^2) + eps)      (64 bits)
- *   y   = bf16(fp32((h * inv) * weight))   (products in 64 bits)
+ *   y   = bf16(fp32(h * inv * weight))     (the products to 2^-47 or better)
  *   fp8bq_rmsnorm_quant:    codes, scales = fp8bq_quant_act(y)
  *   fp8bq_rmsnorm_quant_i8: codes, scales = fp8bq_quant_act_i8(y)
  *
@@ -42,9 +42,10 @@ extern "C" {
  *           residual (it may be R_bf16 or X_bf16 itself: each element is
  *           read before it is written), NULL or ignored without one.
  *   codes, scales: written, as fp8bq_quant_act / fp8bq_quant_act_i8 write
- *           them, which give the same bits for the same y. With 64 bits up
- *           to the rounding of y, the order of the sum shows in no code but
- *           where a value lies within some 2^-50 of a rounding border.
+ *           them, which give the same bits for the same y. The value
+ *           before the rounding of y is kept to 2^-47: the order of the sum
+ *           and of the products shows in no code but where a value lies that
+ *           close to a rounding border.
  * M == 0 or K == 0 is a quick return. NaN or infinite inputs give unspecified
  * codes in their row. Errors: NULL pointer; M < 0, K < 0, K % 128 != 0,
  * K > FP8BQ_NORM_MAX_K, M >= 2^31 or M*K > 2^40; eps not finite or <= 0
@@ -60,8 +61,9 @@ int fp8bq_rmsnorm_quant_i8(int64_t M, int64_t K, const void *X_bf16, const void 
 /*
  * Quantisation to 8-bit integers, one scale per row.
  *
- *   scale = amax / 127 (IEEE fp32 division, amax over the row; 1.0 for an
- *   all-zero row), code = rint(x / scale) (ties to even), in -127 .. 127.
+ *   scale = amax / 127 (IEEE fp32 division, amax over the row; 1.0 where it
+ *   is 0: an all-zero row, or an amax below 2^-143),
+ *   code = rint(x / scale) (ties to even), held to -127 .. 127.
  *
  * fp8bq_quant_act_i8:    A_bf16 [M, K] bf16 -> A_i8 [M, K] int8, A_scales [M]
  *                        fp32: one scale per token.

@@ -9,7 +9,8 @@ the definitions are the ones written out in include/fp8bq_step.h.
 
 * norm: h = bf16(x + r) with the sum in fp32; mean square, root, reciprocal
   and y = (h * inv) * w in fp64, y rounded to fp32 and then to bf16.
-* int8 rows: scale = amax / 127 in fp32, code = rint(x / scale).
+* int8 rows: scale = amax / 127 in fp32 (1 where that is 0), code =
+  rint(x / scale) held to -127 .. 127.
 * product: the integer sums in fp64 (exact below 2^53), rounded to fp32, times
   the fp32 product of the two scales, rounded to bf16.
 * verification: comparisons and sums in Python's whole numbers and Fractions.
@@ -46,8 +47,10 @@ def quant_rows_i8_ref(x):
     """x [M, K] -> (int8 codes [M, K], float32 scales [M])."""
     x = _as_float32(x)
     amax = np.abs(x).max(axis=1).astype(F32)
-    s = np.where(amax > 0, np.divide(amax, F32(127.0), dtype=F32), F32(1.0)).astype(F32)
-    return np.rint(np.divide(x, s[:, None], dtype=F32)).astype(np.int8), s
+    s = np.divide(amax, F32(127.0), dtype=F32)
+    s = np.where(s > 0, s, F32(1.0)).astype(F32)
+    q = np.clip(np.divide(x, s[:, None], dtype=F32), F32(-127.0), F32(127.0))
+    return np.rint(q).astype(np.int8), s
 
 
 def gemm_i8_ref(a_q, a_s, w_q, w_s):

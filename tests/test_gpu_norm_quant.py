@@ -90,6 +90,53 @@ def test_far_magnitudes(scale):
     _check(x, None, _bf16(np.full(384, min(1.0, scale * 1e3))), eps=1.0)
 
 
+def _group_scales(x, exponents):
+    """x with group g of each row times 2^exponents[g % len]."""
+    k = x.shape[1]
+    e = np.repeat(np.resize(exponents, k // 128), 128)
+    return _bf16(x.float().numpy() * np.exp2(e.astype(np.float64)).astype(np.float32))
+
+
+@pytest.mark.parametrize("x_exp,w_exp", [((0, -40, -80, -110), (0,)), ((0,), (0, -60, -120, 60)),
+                                         ((60, 0, -60), (60, -60, 100)), ((100, 64, 30), (0, 27)),
+                                         ((-100, -126), (90, 120)), ((0, -100), (-100, -30))])
+def test_groups_far_apart(x_exp, w_exp):
+    # products of a value and its weight that leave fp32's range, or come near its smallest numbers, in some groups
+    x, r, w = _inputs(5, 1536, 8)
+    x, r = _group_scales(x, x_exp), _group_scales(r, x_exp)
+    w = _group_scales(w[None], w_exp)[0]
+    _check(x, r, w)
+    _check(x, None, w)
+
+
+def test_product_past_fp32_with_a_norm_inside_it():
+    # h w overflows fp32, h inv w does not
+    x, r, w = _inputs(4, 512, 9, 2.0 ** 70)
+    w = _bf16(w.float().numpy() * 2.0 ** 80)
+    _check(x, r, w)
+    _check(x, None, w)
+
+
+@pytest.mark.parametrize("eps", [1e-300, 1e-30, 1e30])
+def test_ends_of_eps(eps):
+    x, r, w = _inputs(4, 384, 10, 1e-3)
+    x[2] = 0.0
+    r[2] = 0.0
+    _check(x, r, w, eps)
+
+
+def test_weight_rows_of_the_smallest_numbers():
+    rng = np.random.default_rng(11)
+    w = np.zeros((200, 128), np.float32)
+    for i in range(200):  # amax = i units of 2^-149: the scale is 0, 1 or 2 of them
+        w[i] = (rng.integers(-i, i + 1, 128).astype(np.int64)).astype(np.float32) * np.float32(2.0 ** -149)
+        w[i, 5] = np.float32(i) * np.float32(2.0 ** -149)
+    codes, scales = fp8bq.quant_weight_i8(to_gpu(w))
+    want_c, want_s = quant_rows_i8_ref(w)
+    _same(codes, want_c)
+    _same(scales, want_s)
+
+
 def test_residual_in_place_and_out_tensor():
     x, r, w = _inputs(9, 640, 5)
     y, h = rmsnorm_ref(x, w, r)

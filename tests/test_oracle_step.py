@@ -131,3 +131,25 @@ def test_verification_rules():
     nothing = np.zeros((1, 4, v), F32)
     t, n = verify_ref(nothing, drafts, u, half)
     assert n[0] == 0 and t[0].tolist() == [-1] * 4
+
+
+def test_int8_rows_of_the_smallest_numbers():
+    x = (np.array([[63, -20], [64, -64], [190, -190], [0, 0]]) * 2.0 ** -149).astype(F32)
+    codes, scales = quant_rows_i8_ref(x)
+    assert scales.tolist() == [1.0, 2.0 ** -149, 2.0 ** -149, 1.0]  # 63 / 127 units round to 0, 190 / 127 to 1
+    assert codes.tolist() == [[0, 0], [64, -64], [127, -127], [0, 0]]
+
+
+def test_two_float_inverse_is_the_64_bit_product():
+    # y = fma(h w, hi, (h w) lo) with hi + lo the inverse: the bf16 of the 64-bit product, as the kernels form it
+    rng = np.random.default_rng(12)
+    h = _bf16(3 * rng.standard_normal(1 << 18))
+    w = _bf16(1 + 0.1 * rng.standard_normal(1 << 18))
+    inv = 1.0 / np.sqrt(rng.random(1 << 18) * 10 + 1e-6)
+    hi = inv.astype(F32)
+    lo = (inv - hi).astype(F32)
+    p = h * w
+    assert np.array_equal(p.astype(np.float64), h.astype(np.float64) * w)
+    # the fma's one rounding: its exact sum is below 2^53 units of the smaller term's last place, but for that sum's own
+    y = (p.astype(np.float64) * hi + (p * lo).astype(np.float64)).astype(F32)
+    assert np.array_equal(bf16_round(y), bf16_round(((h.astype(np.float64) * inv) * w).astype(F32)))
