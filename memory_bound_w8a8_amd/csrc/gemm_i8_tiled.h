@@ -28,12 +28,8 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 
 // 16 x 16 outputs, K = 64: lane l supplies 16 bytes of row l % 16 of the
 // first operand and of column l % 16 of the second, K-slots 16 (l / 16) ..
-// +15; result element i of lane l is row 4 (l / 16) + i, column l % 16.
-__device__ __forceinline__ v4i mfma_16x16x64_i8(const v4u& a, const v4u& b, const v4i& c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), c, 0, 0, 0);
-}
-
-// The same into accumulation registers that stay where they are: from the
+// +15; result element i of lane l is row 4 (l / 16) + i, column l % 16. The
+// sums are in accumulation registers that stay where they are: from the
 // builtin the compiler renames the sums of a loop and moves them back (4 moves
 // per MFMA in a 128 x 128 wave tile). The compiler sees no MFMA here, so the
 // distances it would keep are kept by the callers: 4 or more other MFMAs
@@ -56,8 +52,17 @@ __device__ __forceinline__ void mfma_settle(v4i (&acc)[I][J]) {
 // scales; packed to bf16 by the caller.
 __device__ __forceinline__ float i8_scaled(int sum, float sa, float sw) { return static_cast<float>(sum) * (sa * sw); }
 
-// 16 bytes of C at any element (rows of an odd N start at 2-byte addresses).
+// 16 bytes of C at any element (rows of an odd N start at 2-byte addresses),
+// and 4 sums at any.
 typedef v4u __attribute__((aligned(2))) v4u_at2;
+typedef v4i __attribute__((aligned(4))) v4i_at4;
+
+// Workgroup b of `units` -> unit of work: the workgroups of one XCD (b % 8)
+// take consecutive units, which share operands through its L2.
+__device__ __forceinline__ unsigned xcd_unit(unsigned b, unsigned units) {
+  const unsigned x = b & 7, per = units >> 3, rem = units & 7;
+  return (x < rem ? x * (per + 1) : rem * (per + 1) + (x - rem) * per) + (b >> 3);
+}
 
 // Raw buffer over [base, base + bytes), as its four words, and a direct copy
 // from it to LDS (lane i's 16 bytes land at base + 16 i): per-lane offset
@@ -99,9 +104,11 @@ struct I8Tile {
   static_assert(STAGES >= 2, "the stage being filled is not the one being read");
 };
 
-// part: null, or `split` int32 partial tiles [split][m_rows][n] (part s sums
-// the steps [G s / split, G (s + 1) / split) of G = k / 128).
-template <int BM, int BN, int WM, int WN, int STAGES>
+// SPLIT: the K steps are cut into `split` parts, one workgroup each, whose
+// int32 sums go to part [split][m_rows][n] (part s: the steps [G s / split,
+// G (s + 1) / split) of G = k / 128); gemm_i8_join_kernel adds them. The host
+// keeps tiles x split below 2^24: tiles and steps are counted in 32 bits.
+template <int BM, int BN, int WM, int WN, int STAGES, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_rows, int64_t n, int64_t k, int split,
                                                                      const unsigned char* __restrict__ aq,
                                                                      const float* __restrict__ as,
@@ -119,16 +126,21 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
   const int lrow = lane & 15, quarter = lane >> 4;
   const int wave_m = wave % WM, wave_n = wave / WM;
 
-  const int64_t m_tiles = (m_rows + BM - 1) / BM, n_tiles = (n + BN - 1) / BN;
-  const int64_t units = m_tiles * n_tiles;
-  const int64_t unit = xcd_tile(blockIdx.x, units * split);
-  const int64_t ks = unit / units;
-  int64_t tm, tn;
-  band_tile(unit - ks * units, m_tiles, n_tiles, 8, &tm, &tn);
-  const int64_t m0 = tm * BM, n0 = tn * BN;
-  const int64_t all = k >> 7;
-  const int64_t g_lo = all * ks / split;
-  const int steps = static_cast<int>(all * (ks + 1) / split - g_lo);
+  const unsigned m_tiles = static_cast<unsigned>((m_rows + BM - 1) / BM);
+  const unsigned n_tiles = static_cast<unsigned>((n + BN - 1) / BN);
+  const unsigned all = static_cast<unsigned>(k >> 7);
+  unsigned unit = xcd_unit(blockIdx.x, gridDim.x), ks = 0;
+  if constexpr (SPLIT) {
+    ks = unit / (m_tiles * n_tiles);
+    unit -= ks * (m_tiles * n_tiles);
+  }
+  // bands of 8 token tiles, in which the token tile runs fastest
+  const unsigned band = unit / (8 * n_tiles), at = unit - band * 8 * n_tiles;
+  const unsigned width = m_tiles - 8 * band < 8 ? m_tiles - 8 * band : 8;
+  const unsigned tn = at / width, tm = 8 * band + (at - tn * width);
+  const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
+  const unsigned g_lo = SPLIT ? all * ks / split : 0;
+  const int steps = static_cast<int>(SPLIT ? all * (ks + 1) / split - g_lo : all);
 
   // Copies: this wave's 8-row chunks (tokens first, then weight rows); lane l
   // fetches piece (l % 8) ^ (row & 7) of row l / 8 of the chunk. The buffers
@@ -150,7 +162,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
     const bool tok = BM % (8 * WAVES) == 0 ? 8 * WAVES * q < BM : 8 * (wave + WAVES * q) < BM;
     v4i buf = tok ? a_buf : w_buf;
     buf[2] = s < steps ? buf[2] : 0;
-    buffer_dma16(buf, off[q], static_cast<unsigned>((g_lo + s) * 128), lds_copy + stage * T::kStageBytes + 1024 * WAVES * q);
+    buffer_dma16(buf, off[q], s < steps ? (g_lo + s) * 128 : 0, lds_copy + stage * T::kStageBytes + 1024 * WAVES * q);
   };
 
   // Fragment addresses: row 16 i + lrow of the wave's part, pieces quarter
@@ -218,7 +230,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   mfma_settle(acc);
 
-  if (part != nullptr) {
+  if constexpr (SPLIT) {
     int* dst = part + ks * m_rows * n;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -228,11 +240,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
       for (int i = 0; i < I; ++i) {
         const int64_t col = n0 + T::kTN * wave_n + 16 * i + 4 * quarter;
         int* at = dst + m * n + col;
-        if ((n & 3) == 0 && col + 3 < n) {
-          *reinterpret_cast<v4i*>(at) = acc[i][j];
+        if (col + 3 < n) {
+          *reinterpret_cast<v4i_at4*>(at) = acc[i][j];
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 3; ++e)
             if (col + e < n) at[e] = acc[i][j][e];
         }
       }
@@ -247,6 +259,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
   constexpr int JB = T::kOutRows / 16;    // token fragments at a time
   constexpr int LPR = T::kTN / 8;         // lanes per row
   constexpr int RPI = 64 / LPR;           // rows per store
+  static_assert(LPR * RPI == 64 && T::kOutRows % RPI == 0, "whole waves store whole rows");
+  // Only a tile at an edge of C checks each row and column; its loops are not
+  // unrolled, so that the code (which every launch has to fetch) stays small.
+  const bool whole = m0 + BM <= m_rows && n0 + BN <= n;
   v4f sw[I];
 #pragma unroll
   for (int i = 0; i < I; ++i)
@@ -266,22 +282,26 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
     }
     __builtin_amdgcn_wave_barrier();
     const int lr = lane / LPR, lc = lane % LPR;
+    const int64_t col = n0 + T::kTN * wave_n + 8 * lc;
+    const int64_t m_first = m0 + T::kTM * wave_m + 16 * j0;
+    if (whole) {
+      unsigned short* at = c + (m_first + lr) * n + col;
 #pragma unroll
-    for (int r0 = 0; r0 < T::kOutRows; r0 += RPI) {
-      const int r = r0 + lr;
-      if (RPI * LPR < 64 && lane >= RPI * LPR) continue;
-      if (T::kOutRows % RPI != 0 && r >= T::kOutRows) continue;
-      const v4u v = *reinterpret_cast<const v4u*>(rows + r * T::kOutStride + 16 * lc);
-      const int64_t m = m0 + T::kTM * wave_m + 16 * j0 + r;
-      const int64_t col = n0 + T::kTN * wave_n + 8 * lc;
-      if (m >= m_rows) continue;
-      unsigned short* at = c + m * n + col;
-      if (col + 7 < n) {
-        *reinterpret_cast<v4u_at2*>(at) = v;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (col + e < n) at[e] = static_cast<unsigned short>(v[e >> 1] >> (16 * (e & 1)));
+      for (int r0 = 0; r0 < T::kOutRows; r0 += RPI, at += RPI * n)
+        *reinterpret_cast<v4u_at2*>(at) = *reinterpret_cast<const v4u*>(rows + (r0 + lr) * T::kOutStride + 16 * lc);
+    } else {
+#pragma unroll 1
+      for (int r = lr; r < T::kOutRows; r += RPI) {
+        const int64_t m = m_first + r;
+        if (m >= m_rows) break;
+        unsigned short* at = c + m * n + col;
+        if (col + 7 < n) {
+          *reinterpret_cast<v4u_at2*>(at) = *reinterpret_cast<const v4u*>(rows + r * T::kOutStride + 16 * lc);
+        } else {
+#pragma unroll 1
+          for (int e = 0; col + e < n; ++e)
+            at[e] = *reinterpret_cast<const unsigned short*>(rows + r * T::kOutStride + 16 * lc + 2 * e);
+        }
       }
     }
     __builtin_amdgcn_wave_barrier();
