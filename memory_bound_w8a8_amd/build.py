@@ -3,8 +3,10 @@
     python -m memory_bound_w8a8_amd.build
 
 Each .hip source under csrc/ is compiled to an object in _build/ (in
-parallel), then linked into memory_bound_w8a8_amd/libfp8bq.so. The compile
-always runs (no up-to-date check) so that a stale library is never shipped.
+parallel), then linked into memory_bound_w8a8_amd/libfp8bq.so. Beside it the
+Python module _binding.so is built from binding.cpp (host code only, against
+the installed torch) and linked to that library. The compile always runs (no
+up-to-date check) so that a stale library is never shipped.
 """
 
 import concurrent.futures
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8bq.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = "gfx950"
 HIPCC_FLAGS = [
@@ -59,6 +63,21 @@ def _run(cmd):
     return out
 
 
+def _binding_compile(obj):
+    from torch.utils import cpp_extension
+
+    includes = [f"-I{p}" for p in cpp_extension.include_paths()]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1", f"-I{INCLUDE}", *includes,
+            f"-I{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+
+
+def _binding_link(obj, out):
+    from torch.utils import cpp_extension
+
+    return ["g++", "-shared", "-fPIC", obj, "-o", out, *[f"-L{p}" for p in cpp_extension.library_paths()],
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", f"-L{PKG}", "-l:libfp8bq.so", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(verbose: bool = False) -> str:
     hipcc = _hipcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -66,6 +85,8 @@ def build(verbose: bool = False) -> str:
     objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in sources]
     form = lambda s: [] if s in ACC_FORM_SOURCES else VGPR_FORM  # noqa: E731
     cmds = [[hipcc, *HIPCC_FLAGS, *form(s), "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(sources, objs)]
+    binding_obj = os.path.join(BUILD, "binding.o")
+    cmds.append(_binding_compile(binding_obj))
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(cmds))) as ex:
         for out in ex.map(_run, cmds):
             if verbose and out.strip():
@@ -75,6 +96,11 @@ def build(verbose: bool = False) -> str:
     if verbose and out.strip():
         print(out)
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    out = _run(_binding_link(binding_obj, tmp))
+    if verbose and out.strip():
+        print(out)
+    os.replace(tmp, BINDING)
     return LIB
 
 

@@ -10,7 +10,9 @@ the verification of drafted tokens.
 
 Argument marshalling only, as in the package itself: tensors are checked,
 outputs allocated, and the call enqueued on the current stream of the
-tensors' device.
+tensors' device. Calls whose arguments are in order go through _binding.so
+(csrc/binding.cpp), which does all of it in one step; what it does not take
+comes back to the Python below, which raises, or calls on another device.
 """
 
 import ctypes
@@ -59,12 +61,33 @@ def step_lib():
     return _calls
 
 
-# At a single token the kernels take 3 to 8 us, about as long as a call's way
-# through Python, so that way is kept short: one check per tensor (0.3 us),
-# outputs from empty_like where a tensor of their shape is at hand (1.2 us
-# against 1.7), the raw handle of the current stream (0.1 us; its Stream object
-# takes 2.7).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = torch._C._cuda_getCurrentRawStream  # 0.1 us; a Stream object takes 2.7
+_device = torch._C._cuda_getDevice
+_direct = None
+
+
+def _binding():
+    """The module _binding.so (raises if it has not been built)."""
+    global _direct
+    if _direct is None:
+        step_lib()
+        torch.cuda.init()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("_binding.so is missing or does not load: build it with "
+                              "`python -m memory_bound_w8a8_amd.build`") from e
+        _direct = module
+    return _direct
+
+
+def _done(call, out):
+    """`out` of a _binding call, None where the call was left to Python."""
+    if out.__class__ is int:
+        raise Fp8bqError(call, out)
+    return out
+
+
 _empty, _empty_like = torch.empty, torch.empty_like
 _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
 
@@ -72,7 +95,7 @@ _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.
 def _enqueue(name, index, *args):
     """The call with GPU `index` current and its current stream as last argument."""
     fn = getattr(_calls or step_lib(), name)
-    if index == torch._C._cuda_getDevice():
+    if index == _device():
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -91,6 +114,11 @@ def _on(t, name, dtype, ndim, index):
 
 
 def _rmsnorm(name, x, weight, residual, eps, out_residual, code_dtype):
+    eps = float(eps)
+    module, at = _direct or _binding(), _device()
+    out = _done(name, module.rmsnorm(x, weight, residual, eps, out_residual, code_dtype is _I8, at, _raw_stream(at)))
+    if out is not None:
+        return out
     _need(x, "x", _BF16, 2)
     at = x.get_device()
     _on(weight, "weight", _BF16, 1, at)
@@ -114,10 +142,10 @@ def _rmsnorm(name, x, weight, residual, eps, out_residual, code_dtype):
     codes = _empty_like(x, dtype=code_dtype)
     scales = _empty((m, k // 128) if code_dtype is _U8 else (m,), dtype=_F32, device=x.device)
     if residual is None:
-        _enqueue(name, at, m, k, x.data_ptr(), None, weight.data_ptr(), float(eps), None, codes.data_ptr(),
+        _enqueue(name, at, m, k, x.data_ptr(), None, weight.data_ptr(), eps, None, codes.data_ptr(),
                  scales.data_ptr())
     else:
-        _enqueue(name, at, m, k, x.data_ptr(), residual.data_ptr(), weight.data_ptr(), float(eps), h.data_ptr(),
+        _enqueue(name, at, m, k, x.data_ptr(), residual.data_ptr(), weight.data_ptr(), eps, h.data_ptr(),
                  codes.data_ptr(), scales.data_ptr())
     return codes, scales, h
 
@@ -181,6 +209,10 @@ def gemm_i8(a_q, a_s, w_q, w_s, out=None, workspace=None):
     codes [M, K] and [N, K], fp32 scales [M] and [N], bf16 [M, N]. workspace
     (uint8, on the device): allocated when None and of use; one that is too
     small is not used. The result does not depend on it."""
+    module, at = _direct or _binding(), _device()
+    done = _done("fp8bq_gemm_i8", module.gemm_i8(a_q, a_s, w_q, w_s, out, workspace, at, _raw_stream(at)))
+    if done is not None:
+        return done
     _need(a_q, "a_q", _I8, 2)
     at = a_q.get_device()
     _on(w_q, "w_q", _I8, 2, at)
@@ -221,6 +253,11 @@ def verify_drafts(target_p, drafts, u_accept, u_sample, draft_p=None, draft_len=
     drafts], u_sample fp32 [B], draft_len int32 [B] (None: all). Returns
     (tokens int32 [B, drafts + 1]: the accepted drafts, the drawn token, then
     -1; accepted int32 [B])."""
+    module, at = _direct or _binding(), _device()
+    out = _done("fp8bq_verify_drafts", module.verify_drafts(target_p, drafts, u_accept, u_sample, draft_p, draft_len,
+                                                            workspace, at, _raw_stream(at)))
+    if out is not None:
+        return out
     if not isinstance(target_p, torch.Tensor) or target_p.dtype not in (_F32, _BF16):
         raise TypeError("target_p: expected a float32 or bfloat16 torch.Tensor")
     kind = target_p.dtype

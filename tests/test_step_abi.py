@@ -123,3 +123,19 @@ def test_verify_refusals(L):
         assert call(**bad) == ALIGN, bad
     f = L.fp8bq_verify_workspace_bytes
     assert f(0, 2, 10) == 0 and f(-1, 2, 10) == SHAPE and f(1, 65, 10) == SHAPE and 0 < f(64, 7, 152064) <= 1 << 20
+
+
+def test_binding_leaves_other_tensors_to_python(L):
+    import torch
+
+    from memory_bound_w8a8_amd import _binding
+
+    x, w = torch.ones(2, 128, dtype=torch.bfloat16), torch.ones(128, dtype=torch.bfloat16)
+    assert _binding.rmsnorm(x, w, None, 1e-6, None, False, 0, 0) is None  # not on a GPU
+    a, s = torch.ones(2, 128, dtype=torch.int8), torch.ones(2)
+    assert _binding.gemm_i8(a, s, a, s, None, None, 0, 0) is None
+    p, d, u = torch.ones(2, 2, 5), torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, 1)
+    assert _binding.verify_drafts(p, d, u, s, None, None, None, 0, 0) is None
+    for call in (_binding.rmsnorm, _binding.gemm_i8, _binding.verify_drafts):
+        with pytest.raises(TypeError):
+            call(x)
