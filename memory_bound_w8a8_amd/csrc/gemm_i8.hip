@@ -4,8 +4,8 @@
 // C[m, n] = bf16(fp32(sum_k A[m, k] W[n, k]) * (sa[m] * sw[n])). The sums are
 // exact in 32-bit integers (K < 2^17), so the tiles, the order and the split
 // of K do not show in the result, and the scales are applied once per output.
-// Up to 64 tokens gemm_i8_rows.hip streams the weights; beyond, the tiles
-// below.
+// Up to 64 tokens gemm_i8_rows.hip streams the weights (but for deep K and few
+// rows); beyond, the tiles below.
 #include "device_common.h"
 #include "gemm_i8_tiled.h"
 #include "launch.h"
@@ -17,6 +17,7 @@ namespace {
 
 constexpr int64_t kCUs = 256;
 constexpr int64_t kStreamRows = 64;  // tokens of the weight-streaming kernel
+constexpr int64_t kSplitRows = 32;   // fewer leave half of a 64-row tile empty
 
 // Which tile. With c = ceil(tiles / 256) tiles on the busiest CU and s = K /
 // 128 steps a call takes, in us,
@@ -39,43 +40,57 @@ constexpr Tile kTiles[] = {
     {64, 64, 3.5, 0.182, 1.1, 0.157, 6},
     {64, 128, 4.2, 0.269, 1.5, 0.244, 6},
     {128, 128, 6.2, 0.340, 4.0, 0.467, 8},
-    {128, 256, 6.3, 0.568, 4.3, 0.892, 9},
+    {128, 256, 6.3, 0.568, 4.3, 0.930, 9},
     {256, 256, 8.6, 1.019, 2.9, 1.771, int64_t(1) << 40},  // 8 waves
-    {256, 256, 13.8, 1.007, 7.3, 1.529, int64_t(1) << 40},  // 4 waves: less LDS traffic, a longer end
+    {256, 256, 12.0, 1.000, 7.0, 1.500, int64_t(1) << 40},  // 4 waves: less LDS traffic, a longer start and end
 };
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
 
 // Adding up a split's parts: a launch, and each part's sums written and read.
 constexpr double kJoin = 3.5, kJoinPerByte = 4e-7;
 
+// The weight-streaming kernel: a start, the weights from HBM, and each further
+// 16 tokens' codes, which every CU reads whole through L2 (63 bytes a ns).
+constexpr double kStreamStart = 2.6, kStreamPerByte = 1 / 6.6e6, kStreamPerTokenByte = 1 / 63e3;
+
 struct Plan {
-  int kind;   // index of kTiles
+  int kind;   // index of kTiles, or kStream
   int split;  // parts of K
 };
+constexpr int kStream = -1;
 
 int64_t tile_count(const Tile& t, int64_t m, int64_t n) { return ((m + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn); }
 
 // The K range is split where all tiles of the smallest kind leave most CUs
 // idle: over as many workgroups of at least 4 steps as there are CUs, if the
-// steps saved outweigh the join (128 x 512 x 8704: 15.9 -> 10.4 us).
+// steps saved outweigh the join (128 x 512 x 8704: 15.9 -> 10.4 us), or, up to
+// 64 tokens, if it takes less time than the stream, whose codes weigh most
+// where K is deep (63 x 5120 x 8704: 16.6 -> 13.8 us; 64 x 7168 x 5120 streams
+// in 12.1 and would take 12.7).
 Plan plan_for(int64_t m, int64_t n, int64_t k, bool workspace) {
   const double steps = static_cast<double>(k / 128);
   Plan best{kTileKinds - 1, 1};
   double best_us = 1e300;
-  for (int i = 0; i < kTileKinds; ++i) {
-    const Tile& t = kTiles[i];
-    const int64_t c = (tile_count(t, m, n) + kCUs - 1) / kCUs;
-    if (c > t.rounds) continue;
-    const double us = t.first + steps * t.step + static_cast<double>(c - 1) * (t.more + steps * t.more_step);
-    if (us < best_us) best = Plan{i, 1}, best_us = us;
+  if (m <= kStreamRows) {
+    best.kind = kStream;
+    best_us = kStreamStart + static_cast<double>(n * k) * kStreamPerByte +
+              static_cast<double>((m - 1) / 16 * 16 * k) * kStreamPerTokenByte;
+  } else {
+    for (int i = 0; i < kTileKinds; ++i) {
+      const Tile& t = kTiles[i];
+      const int64_t c = (tile_count(t, m, n) + kCUs - 1) / kCUs;
+      if (c > t.rounds) continue;
+      const double us = t.first + steps * t.step + static_cast<double>(c - 1) * (t.more + steps * t.more_step);
+      if (us < best_us) best = Plan{i, 1}, best_us = us;
+    }
   }
-  if (workspace && best.kind == 0) {
+  if (workspace && m > kSplitRows && best.kind <= 0) {
     const int64_t tiles = tile_count(kTiles[0], m, n), groups = k / 128;
     const int64_t split = kCUs / tiles < groups / 4 ? kCUs / tiles : groups / 4;
     if (split > 1) {
       const double us = kTiles[0].first + static_cast<double>((groups + split - 1) / split) * kTiles[0].step + kJoin +
                         kJoinPerByte * static_cast<double>(8 * split * m * n);
-      if (us < best_us) best.split = static_cast<int>(split);
+      if (us < best_us) best = Plan{0, static_cast<int>(split)};
     }
   }
   return best;
@@ -105,33 +120,34 @@ __global__ __launch_bounds__(256) void gemm_i8_join_kernel(int64_t m_rows, int64
         static_cast<unsigned short>(pack_bf16x2(i8_scaled(sum[e], as[m], ws[col + e]), 0.f) & 0xffffu);
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, bool SPLIT = false>
+template <int BM, int BN, int WM, int WN, int STAGES, bool SPLIT = false, bool FETCH = false>
 hipError_t tile(int64_t m, int64_t n, int64_t k, int split, const void* aq, const float* as, const void* wq,
-                const float* ws, void* c, void* part, hipStream_t stream) {
+                const float* ws, void* c, void* part, const char* name, hipStream_t stream) {
   const int64_t units = tile_count(Tile{BM, BN, 0, 0, 0, 0, 0}, m, n) * split;
   if (units >= int64_t(1) << 23) return hipErrorInvalidValue;  // 2^32 threads of 8 waves
-  hipLaunchKernelGGL((gemm_i8_tiled_kernel<BM, BN, WM, WN, STAGES, SPLIT>), dim3(static_cast<unsigned>(units)),
+  hipLaunchKernelGGL((gemm_i8_tiled_kernel<BM, BN, WM, WN, STAGES, SPLIT, FETCH>), dim3(static_cast<unsigned>(units)),
                      dim3(64 * WM * WN), 0, stream, m, n, k, split, static_cast<const unsigned char*>(aq), as,
                      static_cast<const unsigned char*>(wq), ws, static_cast<unsigned short*>(c),
                      static_cast<int*>(part));
-  dispatch_log("gemm_i8", m, n, k, "gemm_i8_tiled_kernel");
+  dispatch_log("gemm_i8", m, n, k, name);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t gemm_i8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  if (m <= kStreamRows) return 0;
   const Plan p = plan_for(m, n, k, true);
   return p.split > 1 ? 4 * p.split * m * n : 0;
 }
 
 hipError_t launch_gemm_i8(int64_t m, int64_t n, int64_t k, const void* aq, const float* as, const void* wq,
                           const float* ws, void* c, void* workspace, hipStream_t stream) {
-  if (m <= kStreamRows) return launch_gemm_i8_rows(m, n, k, aq, as, wq, ws, c, stream);
   const Plan p = plan_for(m, n, k, workspace != nullptr);
+  if (p.kind == kStream) return launch_gemm_i8_rows(m, n, k, aq, as, wq, ws, c, stream);
   if (p.split > 1) {
-    const hipError_t e = tile<64, 64, 2, 2, 4, true>(m, n, k, p.split, aq, as, wq, ws, c, workspace, stream);
+    const hipError_t e = tile<64, 64, 2, 2, 4, true>(
+        m, n, k, p.split, aq, as, wq, ws, c, workspace,
+        "gemm_i8_tiled_kernel BM=64 BN=64 4 waves 4 stages, K split, + gemm_i8_join_kernel", stream);
     if (e != hipSuccess) return e;
     const int64_t threads = m * ((n + 3) / 4);  // split: below 256 tiles of 64 x 64 outputs
     hipLaunchKernelGGL(gemm_i8_join_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream, m,
@@ -139,12 +155,24 @@ hipError_t launch_gemm_i8(int64_t m, int64_t n, int64_t k, const void* aq, const
     return hipGetLastError();
   }
   switch (p.kind) {
-    case 0: return tile<64, 64, 2, 2, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr, stream);
-    case 1: return tile<64, 128, 1, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr, stream);
-    case 2: return tile<128, 128, 2, 2, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr, stream);
-    case 3: return tile<128, 256, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr, stream);
-    case 4: return tile<256, 256, 2, 4, 2>(m, n, k, 1, aq, as, wq, ws, c, nullptr, stream);
-    default: return tile<256, 256, 2, 2, 2>(m, n, k, 1, aq, as, wq, ws, c, nullptr, stream);
+    case 0:
+      return tile<64, 64, 2, 2, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                   "gemm_i8_tiled_kernel BM=64 BN=64 4 waves 4 stages", stream);
+    case 1:
+      return tile<64, 128, 1, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                   "gemm_i8_tiled_kernel BM=64 BN=128 4 waves 3 stages", stream);
+    case 2:
+      return tile<128, 128, 2, 2, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                   "gemm_i8_tiled_kernel BM=128 BN=128 4 waves 4 stages", stream);
+    case 3:
+      return tile<128, 256, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                   "gemm_i8_tiled_kernel BM=128 BN=256 8 waves 3 stages", stream);
+    case 4:
+      return tile<256, 256, 2, 4, 2>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                   "gemm_i8_tiled_kernel BM=256 BN=256 8 waves 2 stages", stream);
+    default:
+      return tile<256, 256, 2, 2, 2, false, true>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                   "gemm_i8_tiled_kernel BM=256 BN=256 4 waves 2 stages", stream);
   }
 }
 

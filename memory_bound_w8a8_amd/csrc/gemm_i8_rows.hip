@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_i8_rows_kernel(int m_rows, i
   auto copy = [&](int u, int x, int slot) {  // chunk x of the wave's group u; nothing past the last group
     v4i buf = x < MS ? a_buf : w_buf;
     buf[2] = u < count ? buf[2] : 0;
-    const unsigned col = static_cast<unsigned>(g0 + u) * 128;
+    const unsigned col = u < count ? static_cast<unsigned>(g0 + u) * 128 : 0;
     if (x < MS) {
       buffer_dma16(buf, off[x][0], col, ring + slot * kSlotBytes);
       buffer_dma16(buf, off[x][1], col, ring + slot * kSlotBytes + 1024);

@@ -86,6 +86,13 @@ __device__ __forceinline__ void buffer_dma16_once(const v4i& buf, unsigned voff,
                : "memory", "m0");
 }
 
+// 4 bytes a lane (lane i's at base + 4 i).
+__device__ __forceinline__ void buffer_dma4(const v4i& buf, unsigned voff, unsigned soff, unsigned lds_base) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(buf),
+               "s"(soff), "s"(__builtin_amdgcn_readfirstlane(static_cast<int>(lds_base)))
+               : "memory", "m0");
+}
+
 template <int BM, int BN, int WM, int WN, int STAGES>
 struct I8Tile {
   static constexpr int kWaves = WM * WN;
@@ -108,7 +115,16 @@ struct I8Tile {
 // int32 sums go to part [split][m_rows][n] (part s: the steps [G s / split,
 // G (s + 1) / split) of G = k / 128); gemm_i8_join_kernel adds them. The host
 // keeps tiles x split below 2^24: tiles and steps are counted in 32 bits.
-template <int BM, int BN, int WM, int WN, int STAGES, bool SPLIT>
+//
+// FETCH: with 256 x 256 tiles on all CUs a step's lines come from HBM about as
+// late as they may (the copies of a step have half a step to arrive), so each
+// wave also asks for 64 of the lines of the step after them, one word of each
+// into LDS that nobody reads: they are in L2 when their copies go out. Token
+// lines or weight lines by the tile's place, since neighbouring tiles share
+// both. 3465 x 17408 x 5120 263 -> 258 us, 3465 x 8192 x 5120 129 -> 124; a step
+// or three further ahead brings nothing, nor does it with smaller tiles, whose
+// stages are deeper.
+template <int BM, int BN, int WM, int WN, int STAGES, bool SPLIT, bool FETCH>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_rows, int64_t n, int64_t k, int split,
                                                                      const unsigned char* __restrict__ aq,
                                                                      const float* __restrict__ as,
@@ -120,6 +136,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
   constexpr int I = T::kI, J = T::kJ, CH = T::kChunks, WAVES = T::kWaves;
   __shared__ __attribute__((aligned(16))) unsigned char lds[T::kLdsBytes];
   __shared__ float lds_sa[BM], lds_sw[BN];
+  __shared__ __attribute__((aligned(16))) unsigned char lds_unread[FETCH ? 256 * WAVES : 1];
+  static_assert(!FETCH || (BM == 64 * WAVES && BN == 64 * WAVES), "a line of the tile per thread");
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -165,6 +183,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
     buffer_dma16(buf, off[q], s < steps ? (g_lo + s) * 128 : 0, lds_copy + stage * T::kStageBytes + 1024 * WAVES * q);
   };
 
+  const v4i fetch_buf = (tm & 1) != 0 ? a_buf : w_buf;
+  const unsigned fetch_off = static_cast<unsigned>(threadIdx.x * k);
+  const unsigned fetch_lds = lds_addr(lds_unread) + 256 * wave;
+  auto fetch = [&](int s) {  // one word of each line of step s
+    v4i buf = fetch_buf;
+    buf[2] = s < steps ? buf[2] : 0;
+    buffer_dma4(buf, fetch_off, s < steps ? (g_lo + s) * 128 : 0, fetch_lds);
+  };
+
   // Fragment addresses: row 16 i + lrow of the wave's part, pieces quarter
   // (first half) and quarter + 4 (second).
   const int fa = (T::kTM * wave_m + lrow) * 128 + 16 * (quarter ^ (lrow & 7));
@@ -203,6 +230,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
       if constexpr (COPY) {
 #pragma unroll
         for (int q = CH * x / MF; q < CH * (x + 1) / MF; ++q) copy(s, into, q);
+        if constexpr (FETCH) {
+          if (x == MF - 1) fetch(s + 1);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -214,16 +244,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
   for (int s = 0; s < STAGES; ++s)
 #pragma unroll
     for (int q = 0; q < CH; ++q) copy(s, s, q);
+  if constexpr (FETCH) fetch(STAGES);
   for (int i = threadIdx.x; i < BM; i += 64 * WAVES) lds_sa[i] = as[m0 + i < m_rows ? m0 + i : m_rows - 1];
   for (int i = threadIdx.x; i < BN; i += 64 * WAVES) lds_sw[i] = ws[n0 + i < n ? n0 + i : n - 1];
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 1) * CH) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 1) * CH + FETCH) : "memory");
 #pragma unroll
   for (int x = 0; x < I + J; ++x) read(0, 0, x);
 
   for (int s = 0, stage = 0; s < steps; ++s) {
     const int next = stage + 1 < STAGES ? stage + 1 : 0;
     half(Set0{}, std::false_type{}, stage, 0, 0);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * CH) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (CH + FETCH) + FETCH) : "memory");
     half(Set1{}, std::true_type{}, next, s + STAGES, stage);  // past the last step: read, never used
     stage = next;
   }

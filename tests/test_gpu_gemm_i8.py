@@ -60,6 +60,52 @@ def test_larger(m, n, k):
     _check(*_problem(m, n, k, 2))
 
 
+def _check_on_gpu(m, n, k, seed, workspace=None):
+    """The whole output against the exact product in 64 bits, computed on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    a, w = (torch.randint(-128, 128, (rows, k), dtype=torch.int8, device="cuda", generator=g) for rows in (m, n))
+    a_s, w_s = (torch.rand(rows, device="cuda", generator=g) * 0.01 + 1e-4 for rows in (m, n))
+    got = fp8bq.gemm_i8(a, a_s, w, w_s, workspace=workspace)
+    sums = torch.matmul(a.double(), w.double().t().contiguous())
+    want = (sums.float() * (a_s[:, None] * w_s)).to(torch.bfloat16)
+    bad = (got.view(torch.int16) != want.view(torch.int16)).nonzero()
+    assert bad.numel() == 0, f"M={m} N={n} K={k}: {len(bad)} of {got.numel()} differ, first at {bad[0].tolist()}"
+
+
+# each tile shape and both its edges; the last two: 256 x 256 tiles of 4 waves in two rounds, one K step and many
+@pytest.mark.parametrize("m,n,k", [(129, 1000, 2560), (300, 3001, 1280), (129, 15581, 2048), (129, 8192, 5120),
+                                   (257, 8191, 5120), (1499, 5119, 1280), (2047, 7170, 1280), (1025, 17408, 640),
+                                   (3465, 600, 512), (2500, 9001, 5120), (3465, 8195, 5120), (5000, 17409, 128),
+                                   (4097, 16385, 4096)])
+def test_every_tile_shape(m, n, k):
+    _check_on_gpu(m, n, k, 1)
+
+
+# K split over workgroups: parts of unequal length, odd N, few and many parts
+@pytest.mark.parametrize("m,n,k", [(33, 64, 16384), (63, 5120, 8704), (64, 5117, 8704), (65, 512, 5120),
+                                   (128, 513, 8704), (300, 602, 8704), (65, 3, 130944), (1000, 130, 16512)])
+def test_split_of_the_depth(m, n, k):
+    need = fp8bq.gemm_i8_workspace_bytes(m, n, k)
+    assert need >= 8 * m * n and need % (4 * m * n) == 0
+    _check_on_gpu(m, n, k, 2)
+    _check_on_gpu(m, n, k, 3, torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+    _check_on_gpu(m, n, k, 4, torch.full((need - 1,), 255, dtype=torch.uint8, device="cuda"))  # too small: no split
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 400_000, 5632), (300, 400_000, 5632), (70_000, 31_000, 128)])
+def test_offsets_past_31_bits(m, n, k):
+    # weights or outputs of more than 2^31 entries, the last rows against the exact product
+    assert max(n * k, m * n) > 2 ** 31
+    a = torch.randint(-128, 128, (m, k), dtype=torch.int8, device="cuda")
+    w = torch.randint(-128, 128, (n, k), dtype=torch.int8, device="cuda")
+    a_s, w_s = torch.rand(m, device="cuda") + 0.1, torch.rand(n, device="cuda") + 0.1
+    got = fp8bq.gemm_i8(a, a_s, w, w_s)
+    rows, cols = slice(max(0, m - 300), m), slice(n - 300, n)
+    sums = torch.matmul(a[rows].double(), w[cols].double().t().contiguous())
+    want = (sums.float() * (a_s[rows, None] * w_s[cols])).to(torch.bfloat16)
+    assert torch.equal(got[rows, cols], want)
+
+
 @pytest.mark.parametrize("m,n", [(3, 20), (40, 64), (300, 300)])
 def test_deepest_sum_stays_in_32_bits(m, n):
     k = 130944
