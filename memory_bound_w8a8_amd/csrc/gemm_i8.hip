@@ -22,27 +22,30 @@ constexpr int64_t kSplitRows = 32;   // fewer leave half of a 64-row tile empty
 // Which tile. With c = ceil(tiles / 256) tiles on the busiest CU and s = K /
 // 128 steps a call takes, in us,
 //   first + s step + (c - 1) (more + s more_step)
-// for the numbers of each tile: a least-squares fit over 81 shapes of 65 ..
+// for the numbers of each tile: a least-squares fit over 146 shapes of 65 ..
 // 3465 tokens, 512 .. 17408 weight rows and K of 512 .. 17408 drawn evenly over
 // their logarithms (mean error 5%). The smallest prediction picks, over the
-// same shapes, a tile within 0.3% of the fastest one (geometric mean; 9.5% at
-// worst). Small tiles spread few outputs over all CUs, large ones read each
-// operand less often: 65 x 5120 x 5120 takes 11.6 us in 64 x 64 tiles and 19.5
-// in 128 x 128, 1500 x 5120 x 5120 takes 37 in 128 x 256 and 51 in 64 x 128. A
-// CU holds two tiles of the 64-row shapes at a time, hence their small `more`;
-// they are not taken past `rounds`, where the fit ends.
+// same shapes, a tile within 0.4% of the fastest of 17 (geometric mean; 12% at
+// worst).
+//
+// What the numbers say: a CU gets about 90 bytes a ns out of L2, so a step
+// takes (BM + BN) 128 / 90 ns until, at 192 x 256, the MFMAs take as long.
+// Small tiles spread few outputs over all CUs, large ones read each operand
+// less often: 65 x 5120 x 5120 takes 11.6 us in 64 x 64 tiles and 19.5 in 128 x
+// 128, 1500 x 5120 x 5120 takes 37 in 128 x 256 and 51 in 64 x 128. A CU holds
+// two tiles of 64 x 64 at a time, hence their small `more`. The smaller tiles
+// are not taken past `rounds`, where the fit ends.
 struct Tile {
   int bm, bn;
   double first, step, more, more_step;
   int64_t rounds;
 };
+constexpr int64_t kAnyRounds = int64_t(1) << 40;
 constexpr Tile kTiles[] = {
-    {64, 64, 3.5, 0.182, 1.1, 0.157, 6},
-    {64, 128, 4.2, 0.269, 1.5, 0.244, 6},
-    {128, 128, 6.2, 0.340, 4.0, 0.467, 8},
-    {128, 256, 6.3, 0.568, 4.3, 0.930, 9},
-    {256, 256, 8.6, 1.019, 2.9, 1.771, int64_t(1) << 40},  // 8 waves
-    {256, 256, 12.0, 1.000, 7.0, 1.500, int64_t(1) << 40},  // 4 waves: less LDS traffic, a longer start and end
+    {64, 64, 3.3, 0.191, 1.2, 0.167, 6},    {96, 64, 4.0, 0.230, 3.0, 0.239, 6},
+    {64, 128, 3.5, 0.285, 1.6, 0.274, 6},   {128, 128, 4.7, 0.364, 3.5, 0.505, 8},
+    {192, 128, 5.7, 0.455, 5.9, 0.633, 9},  {128, 256, 6.4, 0.576, 5.4, 0.858, 9},
+    {192, 256, 6.9, 0.891, 6.7, 1.309, 9},  {256, 256, 13.5, 1.042, 8.1, 1.531, kAnyRounds},
 };
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
 
@@ -157,22 +160,28 @@ hipError_t launch_gemm_i8(int64_t m, int64_t n, int64_t k, const void* aq, const
   switch (p.kind) {
     case 0:
       return tile<64, 64, 2, 2, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
-                   "gemm_i8_tiled_kernel BM=64 BN=64 4 waves 4 stages", stream);
+                                       "gemm_i8_tiled_kernel BM=64 BN=64 4 waves 4 stages", stream);
     case 1:
-      return tile<64, 128, 1, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
-                   "gemm_i8_tiled_kernel BM=64 BN=128 4 waves 3 stages", stream);
+      return tile<96, 64, 2, 2, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                                       "gemm_i8_tiled_kernel BM=96 BN=64 4 waves 4 stages", stream);
     case 2:
-      return tile<128, 128, 2, 2, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
-                   "gemm_i8_tiled_kernel BM=128 BN=128 4 waves 4 stages", stream);
+      return tile<64, 128, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                                       "gemm_i8_tiled_kernel BM=64 BN=128 8 waves 3 stages", stream);
     case 3:
-      return tile<128, 256, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
-                   "gemm_i8_tiled_kernel BM=128 BN=256 8 waves 3 stages", stream);
+      return tile<128, 128, 2, 4, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                                       "gemm_i8_tiled_kernel BM=128 BN=128 8 waves 4 stages", stream);
     case 4:
-      return tile<256, 256, 2, 4, 2>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
-                   "gemm_i8_tiled_kernel BM=256 BN=256 8 waves 2 stages", stream);
+      return tile<192, 128, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                                       "gemm_i8_tiled_kernel BM=192 BN=128 8 waves 3 stages", stream);
+    case 5:
+      return tile<128, 256, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                                       "gemm_i8_tiled_kernel BM=128 BN=256 8 waves 3 stages", stream);
+    case 6:
+      return tile<192, 256, 2, 4, 2>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                                       "gemm_i8_tiled_kernel BM=192 BN=256 8 waves 2 stages", stream);
     default:
       return tile<256, 256, 2, 2, 2, false, true>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
-                   "gemm_i8_tiled_kernel BM=256 BN=256 4 waves 2 stages", stream);
+                                       "gemm_i8_tiled_kernel BM=256 BN=256 4 waves 2 stages", stream);
   }
 }
 

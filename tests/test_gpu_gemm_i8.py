@@ -72,11 +72,12 @@ def _check_on_gpu(m, n, k, seed, workspace=None):
     assert bad.numel() == 0, f"M={m} N={n} K={k}: {len(bad)} of {got.numel()} differ, first at {bad[0].tolist()}"
 
 
-# each tile shape and both its edges; the last two: 256 x 256 tiles of 4 waves in two rounds, one K step and many
-@pytest.mark.parametrize("m,n,k", [(129, 1000, 2560), (300, 3001, 1280), (129, 15581, 2048), (129, 8192, 5120),
-                                   (257, 8191, 5120), (1499, 5119, 1280), (2047, 7170, 1280), (1025, 17408, 640),
-                                   (3465, 600, 512), (2500, 9001, 5120), (3465, 8195, 5120), (5000, 17409, 128),
-                                   (4097, 16385, 4096)])
+# each tile shape and its edges, one K step and many, one round of tiles and several
+@pytest.mark.parametrize("m,n,k", [(129, 1000, 2560), (129, 8024, 4736), (90, 10001, 640), (302, 15014, 512),
+                                   (346, 12445, 4480), (774, 9616, 1024), (2541, 4565, 1792), (1187, 1576, 1024),
+                                   (300, 3001, 1280), (129, 15581, 2048), (129, 8192, 5120), (257, 8191, 5120),
+                                   (1499, 5119, 1280), (2047, 7170, 1280), (1025, 17408, 640), (3465, 600, 512),
+                                   (2500, 9001, 5120), (3465, 8195, 5120), (5000, 17409, 128), (4097, 16385, 4096)])
 def test_every_tile_shape(m, n, k):
     _check_on_gpu(m, n, k, 1)
 
