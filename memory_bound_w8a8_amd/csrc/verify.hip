@@ -12,10 +12,9 @@
 //   1. verify_sums_kernel: each wave of a row's workgroups sums one part of
 //      it, 16 bytes a lane and load. Every wave finds its sequence's rejection
 //      by itself (two dependent loads); the first one writes it down.
-//   2. verify_draw_kernel: one workgroup of 16 waves per sequence finds the
-//      part that holds the drawn point by a scan over the parts' sums, one a
-//      thread, and scans that part the same way. A part is short enough for
-//      one trip of the workgroup up to 4,000,000 words.
+//   2. verify_draw_kernel: one workgroup of 8 waves per sequence finds the part
+//      that holds the drawn point by a scan over the parts' sums, two a thread,
+//      and scans that part the same way, 16 bytes a thread and trip.
 #include "device_common.h"
 #include "step_launch.h"
 
@@ -27,9 +26,9 @@ typedef unsigned long long u64;
 
 constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / 64;
-constexpr int kDrawThreads = 1024;
+constexpr int kDrawThreads = 512;
 constexpr int kDrawWaves = kDrawThreads / 64;
-constexpr int kMaxParts = kDrawThreads;  // the scan over the parts: one a thread
+constexpr int kMaxParts = 2 * kDrawThreads;  // the scan over the parts: two a thread
 
 struct Verify {
   int n_drafts;
@@ -268,7 +267,8 @@ __global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(Verify a, int
   const int64_t b = blockIdx.x;
   const int t = threadIdx.x;
   const int state = a.state[b];
-  const u64 part = t < a.parts ? a.sums[b * a.parts + t] : 0;
+  const u64* sums = a.sums + b * a.parts;
+  const u64 part0 = 2 * t < a.parts ? sums[2 * t] : 0, part1 = 2 * t + 1 < a.parts ? sums[2 * t + 1] : 0;
   const int kept = t < a.n_drafts ? a.drafts[b * a.n_drafts + t] : -1;
   const float s = a.u_sample[b] * 0x1p32f;
   unsigned s32;
@@ -278,14 +278,13 @@ __global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(Verify a, int
   const int r = state & (kRejected - 1);
 
   u64 total;
-  const u64 run = block_scan(part, slots, &total);
+  const u64 run1 = block_scan(part0 + part1, slots, &total), run0 = run1 - part1;
   int64_t token = -1;
   if (total > 0) {
     const u64 goal = __umul64hi(total, point);  // floor(total * z / 2^32) < total
-    if (run > goal && run - part <= goal) {     // one part: sums rise
-      at_part = t;
-      before_part = run - part;
-    }
+    // one part in all: sums rise
+    if (run0 > goal && run0 - part0 <= goal) at_part = 2 * t, before_part = run0 - part0;
+    if (run1 > goal && run0 <= goal) at_part = 2 * t + 1, before_part = run0;
     __syncthreads();
     const int64_t lo = a.part_words * at_part;
     const int64_t hi = lo + a.part_words < a.v ? lo + a.part_words : a.v;
@@ -301,7 +300,7 @@ __global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(Verify a, int
 }
 
 // Parts of a row: some 8192 waves in all (32 on each CU), at least 256 words
-// a wave (one load a lane), and as many as the second kernel has threads.
+// a wave (one load a lane), and two a thread of the second kernel.
 int part_count(int64_t b, int64_t v) {
   const int64_t fill = (8192 + b - 1) / b, most = (v + 255) / 256;
   const int64_t s = fill < most ? fill : most;
