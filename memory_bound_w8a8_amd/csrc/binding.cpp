@@ -86,7 +86,8 @@ PyObject* rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!is(x, at::kBFloat16, 2, device) || !PyFloat_Check(args[3])) Py_RETURN_NONE;
     const int64_t m = x->size(0), k = x->size(1);
     const at::Tensor *r, *h;
-    if (!shaped(tensor(args[1]), at::kBFloat16, {k}, device) || !optional(args[2], &r, at::kBFloat16, x->sizes(), device) ||
+    if (!shaped(tensor(args[1]), at::kBFloat16, {k}, device) ||
+        !optional(args[2], &r, at::kBFloat16, x->sizes(), device) ||
         !optional(args[4], &h, at::kBFloat16, x->sizes(), device) || (h != nullptr && r == nullptr))
       Py_RETURN_NONE;
     const bool i8 = args[5] == Py_True;
@@ -190,10 +191,13 @@ PyObject* verify_drafts(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+using FastCall = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
+PyCFunction method(FastCall f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
+
 PyMethodDef methods[] = {
-    {"rmsnorm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rmsnorm)), METH_FASTCALL, nullptr},
-    {"gemm_i8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemm_i8)), METH_FASTCALL, nullptr},
-    {"verify_drafts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(verify_drafts)), METH_FASTCALL, nullptr},
+    {"rmsnorm", method(rmsnorm), METH_FASTCALL, nullptr},
+    {"gemm_i8", method(gemm_i8), METH_FASTCALL, nullptr},
+    {"verify_drafts", method(verify_drafts), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

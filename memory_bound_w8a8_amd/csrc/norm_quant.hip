@@ -54,7 +54,8 @@ __device__ __forceinline__ float top_of(unsigned a) {
 // over the workgroup.
 template <int ROT>
 __device__ __forceinline__ unsigned max_rotated(unsigned a) {
-  return max_pair(a, static_cast<unsigned>(__builtin_amdgcn_update_dpp(0, static_cast<int>(a), 0x120 + ROT, 0xf, 0xf, true)));
+  const int other = __builtin_amdgcn_update_dpp(0, static_cast<int>(a), 0x120 + ROT, 0xf, 0xf, true);
+  return max_pair(a, static_cast<unsigned>(other));
 }
 __device__ __forceinline__ unsigned row16_max(unsigned a) {
   return max_rotated<1>(max_rotated<2>(max_rotated<4>(max_rotated<8>(a))));
@@ -178,8 +179,9 @@ __device__ __forceinline__ v2u codes8_e4m3(const v4u& y, float amax, float s) {
 }
 // The same for int8: for every bf16 x in the nine binades below every bf16
 // row maximum the code is the IEEE division's (tested whole), below them 0.
-__device__ __forceinline__ v2u codes8_i8(const float (&f)[8], float amax, float s, const RecipPair& r) {
-  float q[8];
+__device__ __forceinline__ v2u codes8_i8(const v4u& y, float amax, float s, const RecipPair& r) {
+  float f[8], q[8];
+  unpack8(y, f);
   if (amax >= 0x1p-96f) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) q[j] = quotient_e4m3_gemm(f[j], r);
@@ -195,13 +197,16 @@ __device__ __forceinline__ v2u codes8_i8(const float (&f)[8], float amax, float 
 // among them, go out before the first is used. x, r and h may be the same
 // memory: a thread reads its chunks before it writes them.
 //
-// Bound by memory for many rows: 3465 x 5120 with residual to e4m3 moves 125
-// MB in 26.8 us (4.6 TB/s; a copy of 1 GiB reaches 5.2). That took the fp32
-// products and the two-float quotients: with products in 64 bits and IEEE
-// divisions the VALU work (31 operations a value instead of 20) took 35.5 us.
+// Bound by memory for many rows with a residual: 3465 x 5120 to e4m3 moves 125
+// MB in 24 .. 27 us (4.7 .. 5.2 TB/s from box to box; a copy of 1 GiB reaches
+// 5.2). That took the fp32 products and the two-float quotients: with products
+// in 64 bits and IEEE divisions the VALU work (31 operations a value instead of
+// 20) took 35.5 us. Without a residual the VALU work bounds it: 2049 x 8704 to
+// int8 14.6 us (3.7 TB/s), 16.0 with a 64-bit root and divisions in place of
+// the reciprocal root, which each of a row's few waves computes.
 template <int CH, bool RES, bool I8>
-__global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, const unsigned short* x,
-                                                             const unsigned short* r,
+__global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, double inv_k,
+                                                             const unsigned short* x, const unsigned short* r,
                                                              const unsigned short* __restrict__ w, double eps,
                                                              unsigned short* h_out, unsigned char* __restrict__ codes,
                                                              float* __restrict__ scales) {
@@ -251,7 +256,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, c
       for (int j = 0; j < 8; ++j) sum = fma(static_cast<double>(f[j]), static_cast<double>(f[j]), sum);
     }
     sum = block_sum(sum, sums);
-    const Inverse inv(1.0 / sqrt(sum / k + eps));
+    const Inverse inv(rsqrt(sum * inv_k + eps));
 #pragma unroll
     for (int c = 0; c < CH; ++c) stay_packed(h[c]);
     if constexpr (EARLY) {
@@ -304,55 +309,75 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, c
       for (int c = 0; c < CH; ++c) {
         stay_packed(y[c]);
         const int i = t + c * threads;
-        float f[8];
-        unpack8(y[c], f);
-        if (i < chunks) *reinterpret_cast<v2u*>(codes + row * k + 8 * i) = codes8_i8(f, top, s, recip);
+        if (i < chunks) *reinterpret_cast<v2u*>(codes + row * k + 8 * i) = codes8_i8(y[c], top, s, recip);
       }
       if (t == 0) scales[row] = s;
     }
   }
 }
 
-// int8 codes and one scale per row of a bf16 or fp32 matrix.
-template <int CH, typename T>
-__global__ __launch_bounds__(1024) void quant_rows_i8_kernel(int64_t m, int k, const T* __restrict__ a,
+// int8 codes and one scale per row of a bf16 matrix, and of a fp32 one (by the
+// IEEE division: its maxima have 24 bits).
+template <int CH>
+__global__ __launch_bounds__(1024) void quant_rows_i8_kernel(int64_t m, int k, const unsigned short* __restrict__ a,
+                                                             unsigned char* __restrict__ codes,
+                                                             float* __restrict__ scales) {
+  __shared__ unsigned tops[16];
+  const int chunks = k >> 3;
+  for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
+    v4u x[CH];
+    unsigned pair = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = threadIdx.x + c * blockDim.x;
+      x[c] = v4u{0u, 0u, 0u, 0u};
+      if (i < chunks) x[c] = *reinterpret_cast<const v4u*>(a + row * k + 8 * i);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) pair = max_pair(pair, top8(x[c]));
+    const float top = top_of(block_max(pair, tops));
+    const float s = row_scale(top);
+    const RecipPair recip = recip_pair(s);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = threadIdx.x + c * blockDim.x;
+      if (i < chunks) *reinterpret_cast<v2u*>(codes + row * k + 8 * i) = codes8_i8(x[c], top, s, recip);
+    }
+    if (threadIdx.x == 0) scales[row] = s;
+  }
+}
+
+template <int CH>
+__global__ __launch_bounds__(1024) void quant_rows_i8_kernel(int64_t m, int k, const float* __restrict__ a,
                                                              unsigned char* __restrict__ codes,
                                                              float* __restrict__ scales) {
   __shared__ float tops[16];
   const int chunks = k >> 3;
   for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
-    float f[CH][8];
+    v4f f[CH][2];
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = threadIdx.x + c * blockDim.x;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[c][j] = 0.f;
-      if (i < chunks) {
-        const T* p = a + row * k + 8 * i;
-        if constexpr (sizeof(T) == 2) {
-          unpack8(*reinterpret_cast<const v4u*>(p), f[c]);
-        } else {
-          const v4f lo = *reinterpret_cast<const v4f*>(p), hi = *reinterpret_cast<const v4f*>(p + 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[c][j] = lo[j];
-            f[c][4 + j] = hi[j];
-          }
-        }
+      for (int j = 0; j < 2; ++j) {
+        f[c][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (i < chunks) f[c][j] = *reinterpret_cast<const v4f*>(a + row * k + 8 * i + 4 * j);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[c][j]));
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[c][j >> 2][j & 3]));
     }
     top = block_max(top, tops);
     const float s = row_scale(top);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = threadIdx.x + c * blockDim.x;
-      if (i < chunks)
-        *reinterpret_cast<v2u*>(codes + row * k + 8 * i) =
-            v2u{pack4_i8(clamped_i8(f[c][0], s), clamped_i8(f[c][1], s), clamped_i8(f[c][2], s), clamped_i8(f[c][3], s)),
-                pack4_i8(clamped_i8(f[c][4], s), clamped_i8(f[c][5], s), clamped_i8(f[c][6], s), clamped_i8(f[c][7], s))};
+      v2u q;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        q[j] = pack4_i8(clamped_i8(f[c][j][0], s), clamped_i8(f[c][j][1], s), clamped_i8(f[c][j][2], s),
+                        clamped_i8(f[c][j][3], s));
+      if (i < chunks) *reinterpret_cast<v2u*>(codes + row * k + 8 * i) = q;
     }
     if (threadIdx.x == 0) scales[row] = s;
   }
@@ -379,7 +404,8 @@ hipError_t run_rmsnorm(int64_t m, int64_t k, const void* x, const void* r, const
   const int waves = static_cast<int>((k / 8 + 64 * CH - 1) / (64 * CH));
   const auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(row_grid(m)), dim3(64 * waves), 0, stream, m, static_cast<int>(k),
-                       static_cast<const unsigned short*>(x), static_cast<const unsigned short*>(r),
+                       1.0 / static_cast<double>(k), static_cast<const unsigned short*>(x),
+                       static_cast<const unsigned short*>(r),
                        static_cast<const unsigned short*>(w), eps, static_cast<unsigned short*>(h),
                        static_cast<unsigned char*>(codes), scales);
     return hipGetLastError();
@@ -396,11 +422,12 @@ hipError_t run_quant_rows(int64_t m, int64_t k, const void* a, void* codes, floa
                        static_cast<const T*>(a), static_cast<unsigned char*>(codes), scales);
     return hipGetLastError();
   };
+  using Kernel = void (*)(int64_t, int, const T*, unsigned char*, float*);
   switch (rs.chunks) {
-    case 1: return go(quant_rows_i8_kernel<1, T>);
-    case 2: return go(quant_rows_i8_kernel<2, T>);
-    case 4: return go(quant_rows_i8_kernel<4, T>);
-    default: return go(quant_rows_i8_kernel<8, T>);
+    case 1: return go(static_cast<Kernel>(quant_rows_i8_kernel<1>));
+    case 2: return go(static_cast<Kernel>(quant_rows_i8_kernel<2>));
+    case 4: return go(static_cast<Kernel>(quant_rows_i8_kernel<4>));
+    default: return go(static_cast<Kernel>(quant_rows_i8_kernel<8>));
   }
 }
 

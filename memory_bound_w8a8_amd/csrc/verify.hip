@@ -182,7 +182,8 @@ __global__ __launch_bounds__(kSumThreads) void verify_sums_kernel(Verify a) {
   const Row<BF16> row(a, b, r, rejected);
   const int64_t lo = a.part_words * part;
   const int64_t hi = lo + a.part_words < a.v ? lo + a.part_words : a.v;
-  u64 sum = row.q != nullptr ? sum_words<BF16, true>(row, lo, hi, lane, 64) : sum_words<BF16, false>(row, lo, hi, lane, 64);
+  u64 sum = row.q != nullptr ? sum_words<BF16, true>(row, lo, hi, lane, 64)
+                             : sum_words<BF16, false>(row, lo, hi, lane, 64);
   sum = wave_sum(sum);
   if (lane == 0) {
     if (row.certain >= lo && row.certain < hi)

@@ -17,7 +17,8 @@ pytestmark = pytest.mark.gpu
 
 @pytest.fixture(scope="module")
 def example():
-    spec = importlib.util.spec_from_file_location("speculative_step", os.path.join(ROOT, "examples", "speculative_step.py"))
+    path = os.path.join(ROOT, "examples", "speculative_step.py")
+    spec = importlib.util.spec_from_file_location("speculative_step", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     return module
@@ -32,7 +33,7 @@ def test_layers_are_the_oracles(example, monkeypatch):
     tokens = torch.tensor([5, 9, 639, 0, 5], device="cuda")
     seen = []
     product = fp8bq.gemm
-    monkeypatch.setattr(example.fp8bq, "gemm", lambda a_q, a_s, w_q, w_s: seen.append((a_q, a_s)) or product(a_q, a_s, w_q, w_s))
+    monkeypatch.setattr(example.fp8bq, "gemm", lambda *args: seen.append(args) or product(*args))
     p = model.probabilities(tokens)
     assert p.shape == (5, 640) and torch.equal(p[0], p[4])
     x, r = _f32(model.embedding[tokens]), None
@@ -65,6 +66,7 @@ def test_steps_append_the_verified_tokens(example, monkeypatch):
         before = [len(t) for t in texts]
         accepted = example.step(model, texts, 3, generator)
         assert [len(t) - b for t, b in zip(texts, before)] == [n + 1 for n in accepted]
-        assert [t[-n - 1:] for t, n in zip(texts, accepted)] == [row[:n + 1] for row, n in zip(checked[-1][0].tolist(), accepted)]
+        rows = checked[-1][0].tolist()
+        assert [t[-n - 1:] for t, n in zip(texts, accepted)] == [row[:n + 1] for row, n in zip(rows, accepted)]
         assert all(0 <= token < 640 for t in texts for token in t)
     assert len(checked) == 4
