@@ -11,8 +11,8 @@
 // wave's own ring of 4 slots in LDS, without registers and without barriers:
 // chunk c + 3 goes out before chunk c is used, 48 KB in flight per CU. More
 // slots bring nothing while a launch's start grows by 0.1 us for each 16 KB of
-// LDS (7168 x 5120 at 1 token: 7.8 / 8.0 / 8.2 / 8.4 / 8.5 us with 3 / 4 / 6 /
-// 8 / 10 slots; 17408 x 5120 at 64: 22.8 / 22.5 / 22.3 / 22.0 / 22.5), and two
+// LDS (7168 x 5120 at 1 token: 7.3 / 7.5 / 7.6 / 7.7 / 7.9 us with 3 / 4 / 5 / 6
+// / 8 slots; 17408 x 5120 at 64: 20.9 / 20.5 / 20.3 / 20.3 / 20.1), and two
 // workgroups per CU of half the rows are slower (16.6 -> 17.4 us at 17408 x
 // 5120, 5 tokens: twice the activation). A copy instruction reads 8 whole
 // 128-byte lines, the weights' marked as read once (16.9 against 18.1 us

@@ -23,11 +23,25 @@ constexpr float kI8Max = 127.f;
 
 typedef unsigned short v2us __attribute__((ext_vector_type(2)));
 
+// v of the lane ROT further in its DPP row of 16.
+template <int ROT>
+__device__ __forceinline__ int rotated(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x120 + ROT, 0xf, 0xf, true);
+}
+template <int ROT>
+__device__ __forceinline__ double sum_rotated(double v) {
+  const v2u w = __builtin_bit_cast(v2u, v);
+  const v2u o = {static_cast<unsigned>(rotated<ROT>(static_cast<int>(w[0]))),
+                 static_cast<unsigned>(rotated<ROT>(static_cast<int>(w[1])))};
+  return v + __builtin_bit_cast(double, o);
+}
+
 // Sum over the workgroup (every thread gets it). `slots` holds one value per
 // wave; a barrier on both sides lets it be used again.
 __device__ __forceinline__ double block_sum(double v, double* slots) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  v = sum_rotated<1>(sum_rotated<2>(sum_rotated<4>(sum_rotated<8>(v))));
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
   const int waves = blockDim.x >> 6;
   if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -54,8 +68,7 @@ __device__ __forceinline__ float top_of(unsigned a) {
 // over the workgroup.
 template <int ROT>
 __device__ __forceinline__ unsigned max_rotated(unsigned a) {
-  const int other = __builtin_amdgcn_update_dpp(0, static_cast<int>(a), 0x120 + ROT, 0xf, 0xf, true);
-  return max_pair(a, static_cast<unsigned>(other));
+  return max_pair(a, static_cast<unsigned>(rotated<ROT>(static_cast<int>(a))));
 }
 __device__ __forceinline__ unsigned row16_max(unsigned a) {
   return max_rotated<1>(max_rotated<2>(max_rotated<4>(max_rotated<8>(a))));
@@ -438,10 +451,14 @@ hipError_t launch_rmsnorm_quant(int64_t m, int64_t k, const void* x, const void*
   // Three chunks a lane, or one in the shortest rows: fewer waves share a row's
   // barriers and 64-bit root, and several rows stay in flight on a CU. 3465 x
   // 5120 with residual to e4m3 takes 29.6 / 26.8 / 26.8 / 27.8 / 32.7 us with 1
-  // / 2 / 3 / 4 / 6 chunks, 2049 x 5120 without one to int8 16.2 / 11.1 / 10.0 /
-  // 10.2 / 10.6, 3465 x 512 4.9 / 6.0 / 7.3 / 8.7 / 11.5; a single row 4 us.
+  // / 2 / 3 / 4 / 6 chunks, 2049 x 8704 without one to int8 15.0 / 14.4 / 15.4
+  // with 2 / 3 / 4, 3465 x 512 4.9 / 6.0 / 7.3 / 8.7 / 11.5 with 1 / 2 / 3 / 4 /
+  // 6. Where the rows do not fill the CUs, a row's own time counts: two chunks
+  // (256 x 8704 with residual 5.6 / 6.1 / 6.6 us with 2 / 3 / 4, one row 4.2 /
+  // 4.7 / 5.2).
   const int64_t chunks = k / 8;
   if (chunks <= 192) return run_rmsnorm<1>(m, k, x, r, w, eps, h, codes, scales, i8, stream);
+  if (chunks <= 2048 && m <= 256) return run_rmsnorm<2>(m, k, x, r, w, eps, h, codes, scales, i8, stream);
   if (chunks <= 3072) return run_rmsnorm<3>(m, k, x, r, w, eps, h, codes, scales, i8, stream);
   if (chunks <= 4096) return run_rmsnorm<4>(m, k, x, r, w, eps, h, codes, scales, i8, stream);
   return run_rmsnorm<8>(m, k, x, r, w, eps, h, codes, scales, i8, stream);

@@ -66,11 +66,16 @@ _device = torch._C._cuda_getDevice
 _direct = None
 
 
-def _binding():
-    """The module _binding.so (raises if it has not been built)."""
+def _binding(first):
+    """The module _binding.so (raises if it has not been built, or if there is
+    no GPU that the call's first tensor could be on)."""
     global _direct
     if _direct is None:
         step_lib()
+        if not torch.cuda.is_available():
+            if not isinstance(first, torch.Tensor):
+                raise TypeError("expected torch.Tensors")
+            raise ValueError(f"tensors must be on a GPU, got one on {first.device}")
         torch.cuda.init()
         try:
             from . import _binding as module
@@ -115,7 +120,7 @@ def _on(t, name, dtype, ndim, index):
 
 def _rmsnorm(name, x, weight, residual, eps, out_residual, code_dtype):
     eps = float(eps)
-    module, at = _direct or _binding(), _device()
+    module, at = _direct or _binding(x), _device()
     out = _done(name, module.rmsnorm(x, weight, residual, eps, out_residual, code_dtype is _I8, at, _raw_stream(at)))
     if out is not None:
         return out
@@ -209,7 +214,7 @@ def gemm_i8(a_q, a_s, w_q, w_s, out=None, workspace=None):
     codes [M, K] and [N, K], fp32 scales [M] and [N], bf16 [M, N]. workspace
     (uint8, on the device): allocated when None and of use; one that is too
     small is not used. The result does not depend on it."""
-    module, at = _direct or _binding(), _device()
+    module, at = _direct or _binding(a_q), _device()
     done = _done("fp8bq_gemm_i8", module.gemm_i8(a_q, a_s, w_q, w_s, out, workspace, at, _raw_stream(at)))
     if done is not None:
         return done
@@ -253,7 +258,7 @@ def verify_drafts(target_p, drafts, u_accept, u_sample, draft_p=None, draft_len=
     drafts], u_sample fp32 [B], draft_len int32 [B] (None: all). Returns
     (tokens int32 [B, drafts + 1]: the accepted drafts, the drawn token, then
     -1; accepted int32 [B])."""
-    module, at = _direct or _binding(), _device()
+    module, at = _direct or _binding(target_p), _device()
     out = _done("fp8bq_verify_drafts", module.verify_drafts(target_p, drafts, u_accept, u_sample, draft_p, draft_len,
                                                             workspace, at, _raw_stream(at)))
     if out is not None:

@@ -139,3 +139,20 @@ def test_binding_leaves_other_tensors_to_python(L):
     for call in (_binding.rmsnorm, _binding.gemm_i8, _binding.verify_drafts):
         with pytest.raises(TypeError):
             call(x)
+
+
+def test_tensors_off_the_gpu_are_refused(L):
+    import torch
+
+    import memory_bound_w8a8_amd as fp8bq
+
+    x, w = torch.ones(2, 128, dtype=torch.bfloat16), torch.ones(128, dtype=torch.bfloat16)
+    a, s = torch.ones(2, 128, dtype=torch.int8), torch.ones(2)
+    p, d, u = torch.ones(2, 2, 5), torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, 1)
+    for call in (lambda: fp8bq.rmsnorm_quant(x, w), lambda: fp8bq.rmsnorm_quant_i8(x, w, x),
+                 lambda: fp8bq.gemm_i8(a, s, a, s), lambda: fp8bq.verify_drafts(p, d, u, s),
+                 lambda: fp8bq.quant_act_i8(x), lambda: fp8bq.quant_weight_i8(x.float())):
+        with pytest.raises(ValueError, match="on a GPU"):
+            call()
+    with pytest.raises(TypeError):
+        fp8bq.rmsnorm_quant([1.0], w)
