@@ -4,8 +4,8 @@
 // C[m, n] = bf16(fp32(sum_k A[m, k] W[n, k]) * (sa[m] * sw[n])). The sums are
 // exact in 32-bit integers (K < 2^17), so the tiles, the order and the split
 // of K do not show in the result, and the scales are applied once per output.
-// Up to 64 tokens gemm_i8_rows.hip streams the weights (but for deep K and few
-// rows); beyond, the tiles below.
+// Up to 64 tokens gemm_i8_rows.hip streams the weights, but where plan_for finds
+// tiles faster; beyond, the tiles below.
 #include "device_common.h"
 #include "gemm_i8_tiled.h"
 #include "launch.h"
@@ -18,6 +18,7 @@ namespace {
 constexpr int64_t kCUs = 256;
 constexpr int64_t kStreamRows = 64;  // tokens of the weight-streaming kernel
 constexpr int64_t kSplitRows = 32;   // fewer leave half of a 64-row tile empty
+constexpr int64_t kMixedRows = 48;   // from here on a 64-row tile may beat the stream
 
 // Which tile. With c = ceil(tiles / 256) tiles on the busiest CU and s = K /
 // 128 steps a call takes, in us,
@@ -25,14 +26,14 @@ constexpr int64_t kSplitRows = 32;   // fewer leave half of a 64-row tile empty
 // for the numbers of each tile: a least-squares fit over 146 shapes of 65 ..
 // 3465 tokens, 512 .. 17408 weight rows and K of 512 .. 17408 drawn evenly over
 // their logarithms (mean error 5%). The smallest prediction picks, over the
-// same shapes, a tile within 0.4% of the fastest of 17 (geometric mean; 12% at
-// worst).
+// same shapes, a tile within 0.3% of the fastest of these and of 256 x 256 with 8
+// waves (geometric mean; 16% at worst, where one round of the latter wins).
 //
 // What the numbers say: a CU gets about 90 bytes a ns out of L2, so a step
 // takes (BM + BN) 128 / 90 ns until, at 192 x 256, the MFMAs take as long.
 // Small tiles spread few outputs over all CUs, large ones read each operand
-// less often: 65 x 5120 x 5120 takes 11.6 us in 64 x 64 tiles and 19.5 in 128 x
-// 128, 1500 x 5120 x 5120 takes 37 in 128 x 256 and 51 in 64 x 128. A CU holds
+// less often: 65 x 5120 x 5120 takes 11.1 us in 64 x 64 tiles and 18 in 128 x
+// 128, 1500 x 5120 x 5120 takes 35 in 128 x 256 and 51 in 64 x 128. A CU holds
 // two tiles of 64 x 64 at a time, hence their small `more`. The smaller tiles
 // are not taken past `rounds`, where the fit ends.
 struct Tile {
@@ -42,10 +43,11 @@ struct Tile {
 };
 constexpr int64_t kAnyRounds = int64_t(1) << 40;
 constexpr Tile kTiles[] = {
-    {64, 64, 3.3, 0.191, 1.2, 0.167, 6},    {96, 64, 4.0, 0.230, 3.0, 0.239, 6},
-    {64, 128, 3.5, 0.285, 1.6, 0.274, 6},   {128, 128, 4.7, 0.364, 3.5, 0.505, 8},
-    {192, 128, 5.7, 0.455, 5.9, 0.633, 9},  {128, 256, 6.4, 0.576, 5.4, 0.858, 9},
-    {192, 256, 6.9, 0.891, 6.7, 1.309, 9},  {256, 256, 13.5, 1.042, 8.1, 1.531, kAnyRounds},
+    {64, 64, 3.3, 0.172, 1.2, 0.171, 6},   {96, 64, 4.0, 0.215, 3.0, 0.241, 6},
+    {64, 128, 3.5, 0.274, 1.5, 0.265, 6},  {96, 128, 5.5, 0.300, 3.7, 0.391, 6},
+    {128, 128, 4.8, 0.354, 3.3, 0.503, 8}, {192, 128, 5.7, 0.452, 5.0, 0.657, 9},
+    {128, 256, 6.4, 0.567, 4.9, 0.865, 9}, {192, 256, 7.1, 0.867, 5.9, 1.314, 9},
+    {256, 256, 13.5, 1.035, 8.2, 1.500, kAnyRounds},
 };
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
 
@@ -66,10 +68,9 @@ int64_t tile_count(const Tile& t, int64_t m, int64_t n) { return ((m + t.bm - 1)
 
 // The K range is split where all tiles of the smallest kind leave most CUs
 // idle: over as many workgroups of at least 4 steps as there are CUs, if the
-// steps saved outweigh the join (128 x 512 x 8704: 15.9 -> 10.4 us), or, up to
-// 64 tokens, if it takes less time than the stream, whose codes weigh most
-// where K is deep (63 x 5120 x 8704: 16.6 -> 13.8 us; 64 x 7168 x 5120 streams
-// in 12.1 and would take 12.7).
+// steps saved outweigh the join (128 x 512 x 8704: 15.9 -> 10.4 us), also up to
+// 64 tokens, where the stream's codes weigh most with a deep K (63 x 5120 x
+// 8704: 16.6 -> 13.8 us).
 Plan plan_for(int64_t m, int64_t n, int64_t k, bool workspace) {
   const double steps = static_cast<double>(k / 128);
   Plan best{kTileKinds - 1, 1};
@@ -78,6 +79,15 @@ Plan plan_for(int64_t m, int64_t n, int64_t k, bool workspace) {
     best.kind = kStream;
     best_us = kStreamStart + static_cast<double>(n * k) * kStreamPerByte +
               static_cast<double>((m - 1) / 16 * 16 * k) * kStreamPerTokenByte;
+    // One round of 64 x 64 tiles has fewer CUs read the codes, but takes the
+    // weights at 5.2 TB/s at best: 64 x 12000 x 5120 15.9 -> 12.9 us, 64 x 16384 x
+    // 5120 18.7 -> 15.5; 64 x 5120 x 2048 streams in 5.7 and would take 6.4.
+    if (m > kMixedRows && tile_count(kTiles[0], m, n) <= kCUs) {
+      const double tiles = kTiles[0].first + steps * kTiles[0].step;
+      const double read = 1.3 + static_cast<double>(n * k) / 5.2e6;
+      const double us = 1.1 * (tiles > read ? tiles : read);
+      if (us < best_us) best.kind = 0, best_us = us;
+    }
   } else {
     for (int i = 0; i < kTileKinds; ++i) {
       const Tile& t = kTiles[i];
@@ -168,15 +178,18 @@ hipError_t launch_gemm_i8(int64_t m, int64_t n, int64_t k, const void* aq, const
       return tile<64, 128, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
                                        "gemm_i8_tiled_kernel BM=64 BN=128 8 waves 3 stages", stream);
     case 3:
+      return tile<96, 128, 2, 2, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
+                                       "gemm_i8_tiled_kernel BM=96 BN=128 4 waves 4 stages", stream);
+    case 4:
       return tile<128, 128, 2, 4, 4>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
                                        "gemm_i8_tiled_kernel BM=128 BN=128 8 waves 4 stages", stream);
-    case 4:
+    case 5:
       return tile<192, 128, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
                                        "gemm_i8_tiled_kernel BM=192 BN=128 8 waves 3 stages", stream);
-    case 5:
+    case 6:
       return tile<128, 256, 2, 4, 3>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
                                        "gemm_i8_tiled_kernel BM=128 BN=256 8 waves 3 stages", stream);
-    case 6:
+    case 7:
       return tile<192, 256, 2, 4, 2>(m, n, k, 1, aq, as, wq, ws, c, nullptr,
                                        "gemm_i8_tiled_kernel BM=192 BN=256 8 waves 2 stages", stream);
     default:

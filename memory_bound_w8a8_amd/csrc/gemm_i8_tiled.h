@@ -10,7 +10,12 @@
 // directly (dma16). A tile row is 128 bytes, its 16-byte piece c at c ^ (row
 // & 7), so that 8 lanes reading 8 rows hit 8 different bank groups.
 //
-// A step is two halves of K = 64 (one MFMA deep). The fragments of the next
+// In the small tiles of 4 waves (kAhead) all fragments of the next step are
+// read while the MFMAs of this one run: one LDS latency and one barrier a step,
+// which are longer than their 8 .. 24 MFMAs (64 x 64 tiles, 65 x 512 x 5120: 10.4
+// -> 9.4 us; tiles of 8 waves, two on a SIMD, gain nothing).
+//
+// In the others a step is two halves of K = 64 (one MFMA deep). The fragments of the next
 // half are read while the MFMAs of this one run (two register sets). After
 // the first half a wave has read all of the step's stage: one wait and barrier
 // there says that for every wave, and that the next step's stage has landed;
@@ -34,7 +39,9 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // per MFMA in a 128 x 128 wave tile). The compiler sees no MFMA here, so the
 // distances it would keep are kept by the callers: 4 or more other MFMAs
 // between two on the same sums, and mfma_settle() before the first (the sums
-// just written) and after the last (before they are read).
+// just written) and after the last (before they are read). A kernel that keeps
+// sums and spilled values in these registers would move them between: every
+// instance has exactly its sums there.
 __device__ __forceinline__ void mfma_acc_16x16x64_i8(const v4u& a, const v4u& b, v4i& c) {
   asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
@@ -105,6 +112,7 @@ struct I8Tile {
   static constexpr int kOutStride = kTN * 2 + 16;
   static constexpr int kOutBytes = kWaves * kOutRows * kOutStride;
   static constexpr int kLdsBytes = STAGES * kStageBytes > kOutBytes ? STAGES * kStageBytes : kOutBytes;
+  static constexpr bool kAhead = kWaves == 4 && kI * kJ <= 12;
   static_assert((BM + BN) / 8 % kWaves == 0, "every wave issues the same number of copies");
   static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM % 8 == 0, "16-row fragments");
   static_assert(kI * kJ >= 4, "MFMAs between two on the same sums");
@@ -134,6 +142,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
                                                                      int* __restrict__ part) {
   using T = I8Tile<BM, BN, WM, WN, STAGES>;
   constexpr int I = T::kI, J = T::kJ, CH = T::kChunks, WAVES = T::kWaves;
+  constexpr bool AHEAD = T::kAhead;
   __shared__ __attribute__((aligned(16))) unsigned char lds[T::kLdsBytes];
   __shared__ float lds_sa[BM], lds_sw[BN];
   __shared__ __attribute__((aligned(16))) unsigned char lds_unread[FETCH ? 256 * WAVES : 1];
@@ -203,11 +212,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[i][j] = v4i{0, 0, 0, 0};
   mfma_settle(acc);
-  v4u a[2][J], w[2][I];
+  v4u a[AHEAD ? 4 : 2][J], w[AHEAD ? 4 : 2][I];  // register sets: half 0 and 1 of a step, then of the next
 
   auto read = [&](int set, int stage, int x) {  // x: fragment 0 .. I + J - 1
     const unsigned char* at = lds + stage * T::kStageBytes;
-    const int flip = set * 64;  // piece 4 further: bit 6 of the swizzled address
+    const int flip = (set & 1) * 64;  // piece 4 further: bit 6 of the swizzled address
     if (x < I)
       w[set][x] = *reinterpret_cast<const v4u*>(at + (fw ^ flip) + 2048 * x);
     else
@@ -251,12 +260,45 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
 #pragma unroll
   for (int x = 0; x < I + J; ++x) read(0, 0, x);
 
-  for (int s = 0, stage = 0; s < steps; ++s) {
-    const int next = stage + 1 < STAGES ? stage + 1 : 0;
-    half(Set0{}, std::false_type{}, stage, 0, 0);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (CH + FETCH) + FETCH) : "memory");
-    half(Set1{}, std::true_type{}, next, s + STAGES, stage);  // past the last step: read, never used
-    stage = next;
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int x = 0; x < I + J; ++x) read(1, 0, x);
+    // Step s from the sets SET and SET + 1, whose reads are waited for here:
+    // then every wave has read stage `stage`, and the next one has landed.
+    auto step = [&](auto set_c, int s, int stage, int next) {
+      constexpr int set = decltype(set_c)::value, other = 2 - set;
+      constexpr int MF = 2 * I * J, RD = 2 * (I + J), SPAN = MF / 2;
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * CH) : "memory");
+#pragma unroll
+      for (int x = 0; x < MF; ++x) {
+        const int h = x / (I * J), i = x % (I * J) / J, j = x % J;
+#pragma unroll
+        for (int y = RD * x / SPAN; y < RD * (x + 1) / SPAN && y < RD; ++y)
+          read(other + y / (I + J), next, y % (I + J));  // past the last step: read, never used
+        mfma_acc_16x16x64_i8(w[set + h][i], a[set + h][j], acc[i][j]);
+#pragma unroll
+        for (int q = CH * x / MF; q < CH * (x + 1) / MF; ++q) copy(s + STAGES, stage, q);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int stage = 0;
+    for (int s = 0; s < steps; s += 2) {
+      int next = stage + 1 < STAGES ? stage + 1 : 0;
+      step(std::integral_constant<int, 0>{}, s, stage, next);
+      if (s + 1 == steps) break;
+      stage = next;
+      next = stage + 1 < STAGES ? stage + 1 : 0;
+      step(std::integral_constant<int, 2>{}, s + 1, stage, next);
+      stage = next;
+    }
+  } else {
+    for (int s = 0, stage = 0; s < steps; ++s) {
+      const int next = stage + 1 < STAGES ? stage + 1 : 0;
+      half(Set0{}, std::false_type{}, stage, 0, 0);
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * (CH + FETCH) + FETCH) : "memory");
+      half(Set1{}, std::true_type{}, next, s + STAGES, stage);  // past the last step: read, never used
+      stage = next;
+    }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   mfma_settle(acc);

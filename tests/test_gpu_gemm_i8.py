@@ -77,7 +77,8 @@ def _check_on_gpu(m, n, k, seed, workspace=None):
                                    (346, 12445, 4480), (774, 9616, 1024), (2541, 4565, 1792), (1187, 1576, 1024),
                                    (300, 3001, 1280), (129, 15581, 2048), (129, 8192, 5120), (257, 8191, 5120),
                                    (1499, 5119, 1280), (2047, 7170, 1280), (1025, 17408, 640), (3465, 600, 512),
-                                   (2500, 9001, 5120), (3465, 8195, 5120), (5000, 17409, 128), (4097, 16385, 4096)])
+                                   (438, 7051, 3712), (2500, 9001, 5120), (3465, 8195, 5120), (5000, 17409, 128),
+                                   (4097, 16385, 4096)])
 def test_every_tile_shape(m, n, k):
     _check_on_gpu(m, n, k, 1)
 
