@@ -64,10 +64,12 @@ def _run(cmd):
 
 
 def _binding_compile(obj):
+    import torch
     from torch.utils import cpp_extension
 
     includes = [f"-I{p}" for p in cpp_extension.include_paths()]
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1", f"-I{INCLUDE}", *includes,
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", abi, f"-I{INCLUDE}", *includes,
             f"-I{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
 
 

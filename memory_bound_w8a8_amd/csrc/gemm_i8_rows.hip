@@ -1,6 +1,6 @@
 // Weight-streaming int8 product for few tokens (M <= 64), gfx950.
 //
-// Up to some tens of tokens the product reads every weight byte once and is
+// Up to some tens of tokens (plan_for in gemm_i8.hip decides) the product reads every weight byte once and is
 // bound by HBM, so what matters is that every CU streams the same number of
 // bytes and never lets its queue of loads run dry.
 //
