@@ -1,8 +1,8 @@
 // Weight-streaming int8 product for few tokens (M <= 64), gfx950.
 //
-// Up to some tens of tokens (plan_for in gemm_i8.hip decides) the product reads every weight byte once and is
-// bound by HBM, so what matters is that every CU streams the same number of
-// bytes and never lets its queue of loads run dry.
+// Up to some tens of tokens (plan_for in gemm_i8.hip decides) the product reads
+// every weight byte once and is bound by HBM, so what matters is that every CU
+// streams the same number of bytes and never lets its queue of loads run dry.
 //
 // One workgroup per CU owns R = N / 256 weight rows (a multiple of 4, at most
 // 16 TILES), its 8 waves split K. A wave walks its groups of 128 columns; per
