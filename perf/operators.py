@@ -123,10 +123,9 @@ def prepare(case, seed):
 def _norm(s):
     x, r = s["x"], s["residual"]
     h = x if r is None else (x.float() + r.float()).to(torch.bfloat16)
-    # in 64 bits up to the rounding to bf16: a last bit here would move values across its borders
-    wide = h.double()
-    inv = 1.0 / (wide.square().mean(1, keepdim=True) + EPS).sqrt()
-    y = ((wide * inv) * s["weight"].double()).to(torch.bfloat16).float()
+    # the mean square and its root in 64 bits: a last bit here would move values across the codes' rounding borders
+    inv = (1.0 / (h.double().square().mean(1, keepdim=True) + EPS).sqrt()).float()
+    y = ((h.float() * inv) * s["weight"].float()).to(torch.bfloat16).float()
     m, k = y.shape
     top = torch.tensor(E4M3_MAX if s["out"] == "e4m3" else I8_MAX, device=y.device)
     groups = y.view(m, k // GROUP, GROUP) if s["out"] == "e4m3" else y.view(m, 1, k)
