@@ -30,8 +30,9 @@ extern "C" {
  * Residual addition, root-mean-square norm and 8-bit output in one launch.
  *
  *   h   = bf16(x + r)                      (h = x without a residual)
- *   inv = 1 / sqrt(mean_k(h^2) + eps)      (64 bits)
- *   y   = bf16(fp32(h * inv * weight))     (the products to 2^-47 or better)
+ *   inv = fp32(1 / sqrt(mean_k(h^2) + eps)) (mean and root in 64 bits; held
+ *                                          to the largest finite fp32 number)
+ *   y   = bf16((h * inv) * weight)         (fp32 products)
  *   fp8bq_rmsnorm_quant:    codes, scales = fp8bq_quant_act(y)
  *   fp8bq_rmsnorm_quant_i8: codes, scales = fp8bq_quant_act_i8(y)
  *
@@ -42,10 +43,10 @@ extern "C" {
  *           residual (it may be R_bf16 or X_bf16 itself: each element is
  *           read before it is written), NULL or ignored without one.
  *   codes, scales: written, as fp8bq_quant_act / fp8bq_quant_act_i8 write
- *           them, which give the same bits for the same y. The value
- *           before the rounding of y is kept to 2^-47: the order of the sum
- *           and of the products shows in no code but where a value lies that
- *           close to a rounding border.
+ *           them, which give the same bits for the same y. The mean square is
+ *           summed in 64 bits, so the order of the sum shows in no code but
+ *           where the root's inverse lies within about 2^-50 of the border
+ *           between two fp32 numbers (one row in 10^7 or fewer).
  * M == 0 or K == 0 is a quick return. NaN or infinite inputs give unspecified
  * codes in their row. Errors: NULL pointer; M < 0, K < 0, K % 128 != 0,
  * K > FP8BQ_NORM_MAX_K, M >= 2^31 or M*K > 2^40; eps not finite or <= 0

@@ -3,15 +3,18 @@
 //
 // Page 3 (zskr.cn blog), section 3.3, fuses the norm with the quantisation of
 // the linear layer's input; section 2.2 stores weights as INT8. Per row:
-//   h = bf16(x + r), inv = 1 / sqrt(mean(h^2) + eps), y = bf16(h inv w),
+//   h = bf16(x + r), inv = fp32(1 / sqrt(mean(h^2) + eps)), y = bf16((h inv) w),
 // then y is quantised as fp8bq_quant_act does (a scale per 128 columns) or to
 // int8 with a scale per row. Rounding y to bf16 is what the separate norm and
 // quantiser do (their interface is bf16), so the fused codes equal theirs bit
 // for bit; h is rounded because the residual stream is bf16 and the norm has
 // to see what the next layer will see. The sum of squares and the root are in
-// 64 bits, the products as exact as that (Inverse): plain fp32 products round
-// a few values in 10^8 to the other side of a bf16 border, which moves the
-// scale of their group by 2^-8 where they are its maximum.
+// 64 bits, so that inv does not depend on the order of the sum; the two products
+// are rounded to fp32 one after the other, as a norm in fp32 rounds them, which
+// puts y on the other side of a bf16 border than products in 64 bits would in
+// about 5 values in 10^6.
+#include <cfloat>
+
 #include "device_common.h"
 #include "step_launch.h"
 
@@ -124,50 +127,21 @@ __device__ __forceinline__ void unpack8(const v4u& p, float (&x)[8]) {
   }
 }
 
-// 1 / sqrt(mean + eps) as two floats, and whether they may be used (`plain`).
-//
-// y = bf16(fp32((h inv) w)) with the products in 64 bits. In 32 bits the same
-// comes from p = h w, which is exact (8 + 8 bits), and fma(p, hi, p lo): off
-// by 2^-47 of the value before its rounding, where the 64-bit products are
-// off by 2^-52. That needs p, hi and p lo clear of both ends of fp32's range
-// for every value that can get a code other than 0, the ones within 2^-20 of
-// the largest of their scale: hi in 2^-90 .. 2^30 and a largest y of 2^-60 or
-// more, neither infinite nor NaN, see to it (p >= 2^-110, p lo >= 2^-104).
-// Where they do not hold, the row or group is computed in 64 bits.
-struct Inverse {
-  double wide;
-  float hi, lo;
-  bool plain;
-  __device__ __forceinline__ explicit Inverse(double inv) : wide(inv) {
-    hi = static_cast<float>(inv);
-    lo = static_cast<float>(inv - static_cast<double>(hi));
-    plain = hi >= 0x1p-90f && hi <= 0x1p30f;
-  }
-};
-__device__ __forceinline__ bool plain_range(float top) { return top >= 0x1p-60f && top < __builtin_inff(); }
+// 1 / sqrt(v) rounded to fp32. Held to the largest finite number, which only an
+// eps below 2^-256 lets it pass, so that a zero stays a zero. (|h| inv is
+// sqrt(K) at most: only the weights can take y out of range.)
+__device__ __forceinline__ float inverse_root(double v) { return fminf(static_cast<float>(rsqrt(v)), FLT_MAX); }
 
 // Keeps the compiler from carrying unpacked or 64-bit copies of packed values
 // from one use to a later one (four times the registers).
 __device__ __forceinline__ void stay_packed(v4u& p) { asm volatile("" : "+v"(p)); }
 
 // The packed y of 8 packed values h and weights w.
-__device__ __forceinline__ v4u scaled8(const v4u& h, const v4u& w, const Inverse& inv) {
-  const auto one = [&](float f, float g) {
-    const float p = f * g;
-    return fmaf(p, inv.hi, p * inv.lo);
-  };
+__device__ __forceinline__ v4u scaled8(const v4u& h, const v4u& w, float inv) {
   v4u y;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    y[j] = pack_bf16x2(one(bf16_lo(h[j]), bf16_lo(w[j])), one(bf16_hi(h[j]), bf16_hi(w[j])));
-  return y;
-}
-__device__ __forceinline__ v4u scaled8_wide(const v4u& h, const v4u& w, const Inverse& inv) {
-  v4u y;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    y[j] = pack_bf16x2(static_cast<float>((bf16_lo(h[j]) * inv.wide) * bf16_lo(w[j])),
-                       static_cast<float>((bf16_hi(h[j]) * inv.wide) * bf16_hi(w[j])));
+    y[j] = pack_bf16x2((bf16_lo(h[j]) * inv) * bf16_lo(w[j]), (bf16_hi(h[j]) * inv) * bf16_hi(w[j]));
   return y;
 }
 __device__ __forceinline__ unsigned top8(const v4u& y) {
@@ -211,12 +185,10 @@ __device__ __forceinline__ v2u codes8_i8(const v4u& y, float amax, float s, cons
 // memory: a thread reads its chunks before it writes them.
 //
 // Bound by memory for many rows with a residual: 3465 x 5120 to e4m3 moves 125
-// MB in 24 .. 27 us (4.7 .. 5.2 TB/s from box to box; a copy of 1 GiB reaches
-// 5.2). That took the fp32 products and the two-float quotients: with products
-// in 64 bits and IEEE divisions the VALU work (31 operations a value instead of
-// 20) took 35.5 us. Without a residual the VALU work bounds it: 2049 x 8704 to
-// int8 14.6 us (3.7 TB/s), 16.0 with a 64-bit root and divisions in place of
-// the reciprocal root, which each of a row's few waves computes.
+// MB in 23 .. 27 us (4.7 .. 5.4 TB/s; a copy of 1 GiB reaches 5.2, and some of
+// the inputs stay in the memory-side cache at the shorter time). Without a
+// residual 2049 x 8704 to int8 takes 14 .. 16.5 us (3.2 .. 3.8 TB/s): fewer
+// bytes for the same work a value, and 1.6 rounds of rows that the CUs hold.
 template <int CH, bool RES, bool I8>
 __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, double inv_k,
                                                              const unsigned short* x, const unsigned short* r,
@@ -269,7 +241,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, d
       for (int j = 0; j < 8; ++j) sum = fma(static_cast<double>(f[j]), static_cast<double>(f[j]), sum);
     }
     sum = block_sum(sum, sums);
-    const Inverse inv(rsqrt(sum * inv_k + eps));
+    const float inv = inverse_root(sum * inv_k + eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) stay_packed(h[c]);
     if constexpr (EARLY) {
@@ -280,15 +252,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, d
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int i = t + c * threads;
-        v4u wc = EARLY ? wv[EARLY ? c : 0] : weight(c);
-        v4u y = scaled8(h[c], wc, inv);
-        float amax = top_of(row16_max(top8(y)));
-        if (!inv.plain || !plain_range(amax)) {  // whole groups of 16 lanes
-          stay_packed(h[c]);
-          stay_packed(wc);
-          y = scaled8_wide(h[c], wc, inv);
-          amax = top_of(row16_max(top8(y)));
-        }
+        const v4u y = scaled8(h[c], EARLY ? wv[EARLY ? c : 0] : weight(c), inv);
+        const float amax = top_of(row16_max(top8(y)));
         const float s = group_scale(amax);
         if (i < chunks) {
           *reinterpret_cast<v2u*>(codes + row * k + 8 * i) = codes8_e4m3(y, amax, s);
@@ -303,19 +268,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(int64_t m, int k, d
         y[c] = scaled8(h[c], EARLY ? wv[EARLY ? c : 0] : weight(c), inv);
         pair = max_pair(pair, top8(y[c]));
       }
-      float top = top_of(block_max(pair, tops));
-      if (!inv.plain || !plain_range(top)) {  // whole rows
-        pair = 0;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          v4u wc = EARLY ? wv[EARLY ? c : 0] : weight(c);
-          stay_packed(h[c]);
-          stay_packed(wc);
-          y[c] = scaled8_wide(h[c], wc, inv);
-          pair = max_pair(pair, top8(y[c]));
-        }
-        top = top_of(block_max(pair, tops));
-      }
+      const float top = top_of(block_max(pair, tops));
       const float s = row_scale(top);
       const RecipPair recip = recip_pair(s);
 #pragma unroll
@@ -449,13 +402,13 @@ hipError_t run_quant_rows(int64_t m, int64_t k, const void* a, void* codes, floa
 hipError_t launch_rmsnorm_quant(int64_t m, int64_t k, const void* x, const void* r, const void* w, double eps,
                                 void* h, void* codes, float* scales, bool i8, hipStream_t stream) {
   // Three chunks a lane, or one in the shortest rows: fewer waves share a row's
-  // barriers and 64-bit root, and several rows stay in flight on a CU. 3465 x
-  // 5120 with residual to e4m3 takes 29.6 / 26.8 / 26.8 / 27.8 / 32.7 us with 1
-  // / 2 / 3 / 4 / 6 chunks, 2049 x 8704 without one to int8 15.0 / 14.4 / 15.4
-  // with 2 / 3 / 4, 3465 x 512 4.9 / 6.0 / 7.3 / 8.7 / 11.5 with 1 / 2 / 3 / 4 /
-  // 6. Where the rows do not fill the CUs, a row's own time counts: two chunks
-  // (256 x 8704 with residual 5.6 / 6.1 / 6.6 us with 2 / 3 / 4, one row 4.2 /
-  // 4.7 / 5.2).
+  // barriers and 64-bit root, and several rows stay in flight on a CU. With
+  // inputs from HBM, 3465 x 5120 with residual to e4m3 takes 27.8 / 26.4 / 26.7 /
+  // 27.7 / 30.5 us with 1 / 2 / 3 / 4 / 6 chunks, 2049 x 8704 without one to int8
+  // 17.2 / 16.5 / 16.7 with 2 / 3 / 4, 3465 x 512 6.2 / 6.7 / 7.4 / 8.0 / 9.4 with
+  // 1 / 2 / 3 / 4 / 6. Where the rows do not fill the CUs, a row's own time
+  // counts: two chunks (256 x 8704 with residual 7.5 / 8.1 / 8.5 us with 2 / 3 /
+  // 4, one row 3.7 / 4.1 / 4.3).
   const int64_t chunks = k / 8;
   if (chunks <= 192) return run_rmsnorm<1>(m, k, x, r, w, eps, h, codes, scales, i8, stream);
   if (chunks <= 2048 && m <= 256) return run_rmsnorm<2>(m, k, x, r, w, eps, h, codes, scales, i8, stream);

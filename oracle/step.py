@@ -7,8 +7,9 @@ section 2.2 uses INT8 weights; page 1 (SmartX blog), section "single-stream
 optimisation", verifies k drafted tokens per step. The pages give no formulas;
 the definitions are the ones written out in include/fp8bq_step.h.
 
-* norm: h = bf16(x + r) with the sum in fp32; mean square, root, reciprocal
-  and y = (h * inv) * w in fp64, y rounded to fp32 and then to bf16.
+* norm: h = bf16(x + r) with the sum in fp32; mean square, root and reciprocal
+  in fp64, rounded once to fp32 (held to the largest finite number); y =
+  bf16((h * inv) * w) in fp32.
 * int8 rows: scale = amax / 127 in fp32 (1 where that is 0), code =
   rint(x / scale) held to -127 .. 127.
 * product: the integer sums in fp64 (exact below 2^53), rounded to fp32, times
@@ -39,8 +40,8 @@ def rmsnorm_ref(x, w, r=None, eps=1e-6):
     x, w = _as_float32(x), _as_float32(w)
     h = x if r is None else bf16_round(x + _as_float32(r))
     mean = (h.astype(np.float64) ** 2).sum(axis=1, keepdims=True) / x.shape[1]
-    inv = 1.0 / np.sqrt(mean + eps)
-    return bf16_round(((h.astype(np.float64) * inv) * w).astype(F32)), h
+    inv = np.minimum(1.0 / np.sqrt(mean + eps), np.finfo(F32).max).astype(F32)
+    return bf16_round((h * inv) * w), h
 
 
 def quant_rows_i8_ref(x):
