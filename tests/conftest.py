@@ -11,6 +11,14 @@ if TESTS not in sys.path:
     sys.path.insert(0, TESTS)
 
 
+# Tests of the host checks with a call that passes all of them (the misaligned
+# H that a norm without a residual ignores): without a GPU it ends in the device
+# check, with one it would start a kernel on addresses nobody owns.
+# tests/test_made_up_addresses.py finds them; tests/test_gpu_step_limits.py has
+# the same call on tensors.
+MADE_UP_ADDRESSES = {("test_step_abi.py", "test_rmsnorm_refusals")}
+
+
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU and the built HIP library")
 
@@ -26,6 +34,10 @@ def pytest_collection_modifyitems(config, items):
     except Exception:  # pragma: no cover
         have_gpu = False
     if have_gpu:
+        away = pytest.mark.skip(reason="a call of it passes all host checks with made-up addresses; a GPU is present")
+        for item in items:
+            if (item.path.name, getattr(item, "originalname", item.name)) in MADE_UP_ADDRESSES:
+                item.add_marker(away)
         return
     skip = pytest.mark.skip(reason="no GPU in this environment")
     for item in items:
