@@ -164,12 +164,14 @@ __device__ __forceinline__ v2u codes8_e4m3(const v4u& y, float amax, float s) {
   }
   return v2u{encode4_e4m3(q[0], q[1], q[2], q[3]), encode4_e4m3(q[4], q[5], q[6], q[7])};
 }
-// The same for int8: for every bf16 x in the nine binades below every bf16
-// row maximum the code is the IEEE division's (tested whole), below them 0.
+// The same for int8, up to 2^100: from there on the reciprocal's low part nears
+// the subnormal numbers, and above 2^125 it has lost the bits that decide ties (5
+// of the 5.2e8 pairs of bf16 numbers). Up to it the code is the IEEE division's
+// for every bf16 x and every bf16 row maximum (all pairs checked on the host).
 __device__ __forceinline__ v2u codes8_i8(const v4u& y, float amax, float s, const RecipPair& r) {
   float f[8], q[8];
   unpack8(y, f);
-  if (amax >= 0x1p-96f) {
+  if (amax >= 0x1p-96f && amax < 0x1p100f) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) q[j] = quotient_e4m3_gemm(f[j], r);
   } else {
