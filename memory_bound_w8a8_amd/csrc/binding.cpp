@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "fp8bq_step.h"
@@ -49,17 +50,14 @@ PyObject* pair_of(PyObject* a, PyObject* b) {
   return out;
 }
 
-// A C++ exception (out of memory) becomes a Python one.
+// A C++ exception becomes the Python one that torch makes of it: an output that
+// does not fit the device raises torch.OutOfMemoryError, as in the Python of
+// step.py.
 template <typename F>
 PyObject* guarded(F f) {
-  try {
-    return f();
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
-  }
-  return nullptr;
+  HANDLE_TH_ERRORS
+  return f();
+  END_HANDLE_TH_ERRORS
 }
 
 // The device and the stream a call ends with.
