@@ -43,9 +43,11 @@ __device__ __forceinline__ v4i mfma_16x16x64_i8(const v4u& a, const v4u& b, cons
 // 8 bytes of C at any element.
 typedef v2u __attribute__((aligned(2))) v2u_at2;
 
-// MS: 16-token blocks; TILES: 16-row tiles.
+// MS: 16-token blocks; TILES: 16-row tiles. n: weight rows of this launch; ldc:
+// those of C.
 template <int MS, int TILES>
-__global__ __launch_bounds__(64 * kWaves) void gemm_i8_rows_kernel(int m_rows, int64_t n, int64_t k, int rows_per_wg,
+__global__ __launch_bounds__(64 * kWaves) void gemm_i8_rows_kernel(int m_rows, int64_t n, int64_t k, int64_t ldc,
+                                                                   int rows_per_wg,
                                                                    const unsigned char* __restrict__ aq,
                                                                    const float* __restrict__ as,
                                                                    const unsigned char* __restrict__ wq,
@@ -169,7 +171,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_i8_rows_kernel(int m_rows, i
       if (m >= m_rows || r >= rows) continue;
       const v2u p = {pack_bf16x2(i8_scaled(sum[0], sa[y], sw[y][0]), i8_scaled(sum[1], sa[y], sw[y][1])),
                      pack_bf16x2(i8_scaled(sum[2], sa[y], sw[y][2]), i8_scaled(sum[3], sa[y], sw[y][3]))};
-      unsigned short* dst = c + m * n + r_begin + r;
+      unsigned short* dst = c + m * ldc + r_begin + r;
       if (r + 3 < rows) {
         *reinterpret_cast<v2u_at2*>(dst) = p;
       } else {
@@ -182,25 +184,37 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_i8_rows_kernel(int m_rows, i
   }
 }
 
+struct Launch {
+  dim3 grid;
+  int rows_per_wg;
+  int64_t m, n, k, ldc;
+  const unsigned char* aq;
+  const float* as;
+  const unsigned char* wq;
+  const float* ws;
+  unsigned short* c;
+  hipStream_t stream;
+};
+
 template <int MS, int TILES>
-void run(const dim3& grid, int rows_per_wg, int64_t m, int64_t n, int64_t k, const void* aq, const float* as,
-         const void* wq, const float* ws, void* c, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_i8_rows_kernel<MS, TILES>), grid, dim3(64 * kWaves), 0, stream, static_cast<int>(m), n, k,
-                     rows_per_wg, static_cast<const unsigned char*>(aq), as, static_cast<const unsigned char*>(wq), ws,
-                     static_cast<unsigned short*>(c));
+void run(const Launch& a) {
+  hipLaunchKernelGGL((gemm_i8_rows_kernel<MS, TILES>), a.grid, dim3(64 * kWaves), 0, a.stream, static_cast<int>(a.m),
+                     a.n, a.k, a.ldc, a.rows_per_wg, a.aq, a.as, a.wq, a.ws, a.c);
 }
 
 template <int MS>
-void run_tiles(int tiles, const dim3& grid, int rows_per_wg, int64_t m, int64_t n, int64_t k, const void* aq,
-               const float* as, const void* wq, const float* ws, void* c, hipStream_t stream) {
-  switch (tiles) {
-    case 1: return run<MS, 1>(grid, rows_per_wg, m, n, k, aq, as, wq, ws, c, stream);
-    case 2: return run<MS, 2>(grid, rows_per_wg, m, n, k, aq, as, wq, ws, c, stream);
-    case 3: return run<MS, 3>(grid, rows_per_wg, m, n, k, aq, as, wq, ws, c, stream);
-    case 4: return run<MS, 4>(grid, rows_per_wg, m, n, k, aq, as, wq, ws, c, stream);
-    default: return run<MS, 5>(grid, rows_per_wg, m, n, k, aq, as, wq, ws, c, stream);
+void run_tiles(const Launch& a) {
+  switch ((a.rows_per_wg + 15) / 16) {
+    case 1: return run<MS, 1>(a);
+    case 2: return run<MS, 2>(a);
+    case 3: return run<MS, 3>(a);
+    case 4: return run<MS, 4>(a);
+    default: return run<MS, 5>(a);
   }
 }
+
+// Workgroups of a launch: fewer than 2^32 threads.
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 23) - 1;
 
 }  // namespace
 
@@ -210,20 +224,27 @@ hipError_t launch_gemm_i8_rows(int64_t m, int64_t n, int64_t k, const void* aq, 
   const int64_t rounds = (n + kCUs * 16 * kMaxRowTiles - 1) / (kCUs * 16 * kMaxRowTiles);
   const int64_t even = (n + kCUs * rounds - 1) / (kCUs * rounds);
   const int rows = static_cast<int>((even + 3) / 4 * 4);
-  const int64_t wgs = (n + rows - 1) / rows;
-  if (m > 64 || wgs >= int64_t(1) << 23) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(wgs));
-  const int tiles = (rows + 15) / 16;
-  if (m <= 16)
-    run_tiles<1>(tiles, grid, rows, m, n, k, aq, as, wq, ws, c, stream);
-  else if (m <= 32)
-    run_tiles<2>(tiles, grid, rows, m, n, k, aq, as, wq, ws, c, stream);
-  else if (m <= 48)
-    run_tiles<3>(tiles, grid, rows, m, n, k, aq, as, wq, ws, c, stream);
-  else
-    run_tiles<4>(tiles, grid, rows, m, n, k, aq, as, wq, ws, c, stream);
+  if (m > 64) return hipErrorInvalidValue;
+  // One launch, but from about 671 million weight rows on
+  const int64_t most = rows * kMaxWorkgroups;
+  for (int64_t r0 = 0; r0 < n; r0 += most) {
+    const int64_t here = n - r0 < most ? n - r0 : most;
+    const Launch a{dim3(static_cast<unsigned>((here + rows - 1) / rows)), rows, m, here, k, n,
+                   static_cast<const unsigned char*>(aq), as, static_cast<const unsigned char*>(wq) + r0 * k, ws + r0,
+                   static_cast<unsigned short*>(c) + r0, stream};
+    if (m <= 16)
+      run_tiles<1>(a);
+    else if (m <= 32)
+      run_tiles<2>(a);
+    else if (m <= 48)
+      run_tiles<3>(a);
+    else
+      run_tiles<4>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   dispatch_log("gemm_i8", m, n, k, "gemm_i8_rows_kernel");
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace fp8bq

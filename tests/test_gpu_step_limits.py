@@ -47,3 +47,22 @@ def test_output_too_large_to_allocate(way):
     a, s = torch.ones(1 << 20, 128, dtype=torch.int8, device="cuda"), torch.ones(1 << 20, device="cuda")
     with pytest.raises(torch.OutOfMemoryError):
         fp8bq.gemm_i8(a, s, a, s)
+
+
+def test_more_weight_rows_than_one_grid():
+    # 2^23 workgroups of 80 rows and some more, at the least depth: 86 GB of weights
+    n, k = 80 * (1 << 23) + 1003, 128
+    w = torch.zeros(n, k, dtype=torch.int8, device="cuda")
+    marks = torch.tensor([0, 79, 80 * (1 << 22), 80 * (1 << 23) - 81, 80 * (1 << 23) - 80, 80 * (1 << 23) - 1,
+                          80 * (1 << 23), n - 1], device="cuda")
+    w[marks] = torch.arange(1, len(marks) + 1, device="cuda", dtype=torch.int8)[:, None]
+    w_s = torch.ones(n, device="cuda")
+    w_s[marks] = 0.5
+    a, a_s = torch.ones(2, k, dtype=torch.int8, device="cuda"), torch.tensor([1.0, 2.0], device="cuda")
+    a[1, ::2] = 0
+    c = fp8bq.gemm_i8(a, a_s, w, w_s)
+    want = torch.arange(1, len(marks) + 1, device="cuda") * 64.0  # 128 x 0.5, and 64 x 0.5 x 2
+    assert c.shape == (2, n)
+    for row in range(2):
+        assert torch.equal(c[row, marks].float(), want)
+        assert int((c[row] != 0).sum()) == len(marks)
