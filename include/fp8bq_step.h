@@ -98,8 +98,8 @@ int fp8bq_quant_weight_i8(int64_t N, int64_t K, const float *W_f32, void *W_i8, 
  *                    below it (0 included) it is not. Same result.
  * M == 0 or N == 0 is a quick return; K == 0 writes zeros. Errors: NULL
  * pointer; negative size; K % 128 != 0; K > FP8BQ_GEMM_I8_MAX_K (sums then
- * leave 32 bits); M*K, N*K or M*N > 2^40; M or N >= 2^31; workspace_bytes
- * < 0; codes, C_bf16 or workspace not 16-B aligned, scales not 4-B aligned;
+ * leave 32 bits); M*K, N*K or M*N > 2^40; M or N >= 2^31; M > 64 with 2^23
+ * or more tiles of 256 tokens x 256 weight rows; workspace_bytes < 0; codes, C_bf16 or workspace not 16-B aligned, scales not 4-B aligned;
  * device not gfx950.
  *
  * fp8bq_gemm_i8_workspace_bytes: the scratch the plan for (M, N, K) takes

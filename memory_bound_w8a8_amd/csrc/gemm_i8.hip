@@ -109,6 +109,10 @@ Plan plan_for(int64_t m, int64_t n, int64_t k, bool workspace) {
   return best;
 }
 
+// Workgroups of a launch stay below 2^32 threads of 8 waves. Only 256 x 256 tiles
+// are taken that often (the others within `rounds`).
+constexpr int64_t kMaxUnits = int64_t(1) << 23;
+
 // Adds the parts of a split: 4 outputs a thread.
 __global__ __launch_bounds__(256) void gemm_i8_join_kernel(int64_t m_rows, int64_t n, int split,
                                                            const int* __restrict__ part, const float* __restrict__ as,
@@ -137,7 +141,7 @@ template <int BM, int BN, int WM, int WN, int STAGES, bool SPLIT = false, bool F
 hipError_t tile(int64_t m, int64_t n, int64_t k, int split, const void* aq, const float* as, const void* wq,
                 const float* ws, void* c, void* part, const char* name, hipStream_t stream) {
   const int64_t units = tile_count(Tile{BM, BN, 0, 0, 0, 0, 0}, m, n) * split;
-  if (units >= int64_t(1) << 23) return hipErrorInvalidValue;  // 2^32 threads of 8 waves
+  if (units >= kMaxUnits) return hipErrorInvalidValue;
   hipLaunchKernelGGL((gemm_i8_tiled_kernel<BM, BN, WM, WN, STAGES, SPLIT, FETCH>), dim3(static_cast<unsigned>(units)),
                      dim3(64 * WM * WN), 0, stream, m, n, k, split, static_cast<const unsigned char*>(aq), as,
                      static_cast<const unsigned char*>(wq), ws, static_cast<unsigned short*>(c),
@@ -147,6 +151,10 @@ hipError_t tile(int64_t m, int64_t n, int64_t k, int split, const void* aq, cons
 }
 
 }  // namespace
+
+bool gemm_i8_fits(int64_t m, int64_t n) {
+  return m <= kStreamRows || tile_count(kTiles[kTileKinds - 1], m, n) < kMaxUnits;
+}
 
 int64_t gemm_i8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   const Plan p = plan_for(m, n, k, true);

@@ -122,7 +122,7 @@ struct I8Tile {
 // SPLIT: the K steps are cut into `split` parts, one workgroup each, whose
 // int32 sums go to part [split][m_rows][n] (part s: the steps [G s / split,
 // G (s + 1) / split) of G = k / 128); gemm_i8_join_kernel adds them. The host
-// keeps tiles x split below 2^24: tiles and steps are counted in 32 bits.
+// keeps tiles x split below 2^23: tiles and steps are counted in 32 bits.
 //
 // FETCH: with 256 x 256 tiles on all CUs a step's lines come from HBM about as
 // late as they may (the copies of a step have half a step to arrive), so each

@@ -42,7 +42,8 @@ int rmsnorm_quant(int64_t M, int64_t K, const void* X, const void* R, const void
 int check_gemm_i8_sizes(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0 || K % 128 != 0 || K > FP8BQ_GEMM_I8_MAX_K || M > kMaxIndex || N > kMaxIndex)
     return FP8BQ_ERR_SHAPE;
-  if (!product_ok(M, K) || !product_ok(N, K) || !product_ok(M, N)) return FP8BQ_ERR_SHAPE;
+  if (!product_ok(M, K) || !product_ok(N, K) || !product_ok(M, N) || !fp8bq::gemm_i8_fits(M, N))
+    return FP8BQ_ERR_SHAPE;
   return FP8BQ_OK;
 }
 

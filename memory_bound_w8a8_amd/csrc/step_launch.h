@@ -17,7 +17,8 @@ hipError_t launch_quant_rows_i8_f32(int64_t n, int64_t k, const float* w, void* 
                                     hipStream_t stream);
 
 // gemm_i8.hip. workspace: gemm_i8_workspace_bytes(m, n, k) bytes, or null for
-// the plan without one.
+// the plan without one. gemm_i8_fits: whether one grid takes the tiles.
+bool gemm_i8_fits(int64_t m, int64_t n);
 int64_t gemm_i8_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_gemm_i8(int64_t m, int64_t n, int64_t k, const void* aq, const float* as, const void* wq,
                           const float* ws, void* c, void* workspace, hipStream_t stream);

@@ -11,7 +11,7 @@ import pytest
 import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-FILES = ["test_abi.py", "test_step_abi.py"]
+FILES = ["test_abi.py", "test_step_abi.py", "test_step_limits.py"]
 
 
 def _session(word, *args, **env):
