@@ -1,5 +1,7 @@
 // C ABI of the operators of include/fp8bq_step.h: host-side validation and
 // dispatch.
+#include <cmath>
+
 #include "api_checks.h"
 #include "fp8bq_step.h"
 #include "launch.h"
@@ -25,7 +27,7 @@ int rmsnorm_quant(int64_t M, int64_t K, const void* X, const void* R, const void
                   void* codes, float* scales, bool i8, void* stream) {
   int st = check_rows(M, K);
   if (st != FP8BQ_OK) return st;
-  if (!(eps > 0.0) || eps > 1e30) return FP8BQ_ERR_VALUE;
+  if (!(eps > 0.0) || std::isinf(eps)) return FP8BQ_ERR_VALUE;
   if (M == 0 || K == 0) return FP8BQ_OK;
   if (X == nullptr || weight == nullptr || codes == nullptr || scales == nullptr) return FP8BQ_ERR_NULL;
   if (R == nullptr) H = nullptr;

@@ -66,3 +66,9 @@ def test_more_weight_rows_than_one_grid():
     for row in range(2):
         assert torch.equal(c[row, marks].float(), want)
         assert int((c[row] != 0).sum()) == len(marks)
+
+
+def test_largest_eps():
+    x, w = torch.ones(3, 256, dtype=BF16, device="cuda"), torch.ones(256, dtype=BF16, device="cuda")
+    codes, scales, _ = fp8bq.rmsnorm_quant(x, w, eps=1e300)  # 1 / sqrt(eps) is 0 in fp32
+    assert not codes.any() and bool((scales == 1).all())

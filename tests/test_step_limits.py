@@ -33,3 +33,11 @@ def test_product_with_more_tiles_than_one_grid_is_a_shape(L):
     for m, n in ((256 * (2 ** 23 - 1), 100), (256 * 2 ** 11, 256 * (2 ** 12 - 1)), (64, 2 ** 31 - 1), (1, 2 ** 31 - 1)):
         assert call(m, n) == ALIGN, (m, n)
         assert L.fp8bq_gemm_i8_workspace_bytes(m, n, 128) >= 0, (m, n)
+
+
+@pytest.mark.parametrize("name", ["fp8bq_rmsnorm_quant", "fp8bq_rmsnorm_quant_i8"])
+def test_every_finite_eps_serves(L, name):
+    # the bad alignment of the codes is looked at after eps
+    for eps, status in ((5e-324, ALIGN), (1e30, ALIGN), (2e30, ALIGN), (1.7e308, ALIGN), (float("inf"), VALUE),
+                        (float("nan"), VALUE), (0.0, VALUE), (-1e300, VALUE)):
+        assert getattr(L, name)(1, 128, P, None, P, eps, None, P + 2, P, None) == status, eps
