@@ -47,7 +47,8 @@ extern "C" {
  *           summed in 64 bits, so the order of the sum shows in no code but
  *           where the root's inverse lies within about 2^-50 of the border
  *           between two fp32 numbers (one row in 10^7 or fewer).
- * M == 0 or K == 0 is a quick return. NaN or infinite inputs give unspecified
+ * M == 0 or K == 0 is a quick return that writes nothing (the scales of int8
+ * rows without columns among it). NaN or infinite inputs give unspecified
  * codes in their row. Errors: NULL pointer; M < 0, K < 0, K % 128 != 0,
  * K > FP8BQ_NORM_MAX_K, M >= 2^31 or M*K > 2^40; eps not finite or <= 0
  * (FP8BQ_ERR_VALUE); X_bf16, R_bf16, weight, H_bf16 or codes not 16-B
@@ -71,7 +72,7 @@ int fp8bq_rmsnorm_quant_i8(int64_t M, int64_t K, const void *X_bf16, const void 
  * fp8bq_quant_weight_i8: W_f32 [N, K] fp32 -> W_i8 [N, K] int8, W_scales [N]
  *                        fp32: one scale per output channel.
  * Bit-exact with the definition for finite inputs. M == 0, N == 0 or K == 0
- * is a quick return. Errors: as fp8bq_quant_act, K > FP8BQ_NORM_MAX_K, and
+ * is a quick return that writes nothing. Errors: as fp8bq_quant_act, K > FP8BQ_NORM_MAX_K, and
  * M, N >= 2^31.
  */
 int fp8bq_quant_act_i8(int64_t M, int64_t K, const void *A_bf16, void *A_i8, float *A_scales, void *stream);

@@ -89,6 +89,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         !optional(args[4], &h, at::kBFloat16, x->sizes(), device) || (h != nullptr && r == nullptr))
       Py_RETURN_NONE;
     const bool i8 = args[5] == Py_True;
+    if (i8 && k == 0) Py_RETURN_NONE;  // the call writes no scales then: step.py does
     at::Tensor h_new;
     if (r != nullptr && h == nullptr) {
       h_new = empty(x->sizes(), at::kBFloat16, *x);

@@ -118,6 +118,12 @@ def _on(t, name, dtype, ndim, index):
     raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
 
 
+def _row_scales(rows, k, device):
+    """Room for a scale per row; without columns the calls write none, and the
+    scale of a row of nothing is that of a row of zeros."""
+    return _empty((rows,), dtype=_F32, device=device) if k else torch.ones((rows,), dtype=_F32, device=device)
+
+
 def _rmsnorm(name, x, weight, residual, eps, out_residual, code_dtype):
     eps = float(eps)
     module, at = _direct or _binding(x), _device()
@@ -145,7 +151,10 @@ def _rmsnorm(name, x, weight, residual, eps, out_residual, code_dtype):
     elif out_residual is not None:
         raise ValueError("out_residual needs a residual")
     codes = _empty_like(x, dtype=code_dtype)
-    scales = _empty((m, k // 128) if code_dtype is _U8 else (m,), dtype=_F32, device=x.device)
+    if code_dtype is _U8:
+        scales = _empty((m, k // 128), dtype=_F32, device=x.device)
+    else:
+        scales = _row_scales(m, k, x.device)
     if residual is None:
         _enqueue(name, at, m, k, x.data_ptr(), None, weight.data_ptr(), eps, None, codes.data_ptr(),
                  scales.data_ptr())
@@ -172,7 +181,7 @@ def rmsnorm_quant_i8(x, weight, residual=None, eps=1e-6, out_residual=None):
 def _quant_rows(name, x):
     rows, k = x.shape
     codes = _empty_like(x, dtype=_I8)
-    scales = _empty((rows,), dtype=_F32, device=x.device)
+    scales = _row_scales(rows, k, x.device)
     _enqueue(name, x.get_device(), rows, k, x.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return codes, scales
 

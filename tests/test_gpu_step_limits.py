@@ -72,3 +72,14 @@ def test_largest_eps():
     x, w = torch.ones(3, 256, dtype=BF16, device="cuda"), torch.ones(256, dtype=BF16, device="cuda")
     codes, scales, _ = fp8bq.rmsnorm_quant(x, w, eps=1e300)  # 1 / sqrt(eps) is 0 in fp32
     assert not codes.any() and bool((scales == 1).all())
+
+
+def test_depth_zero_gives_scales_of_one(way):
+    # the scale of a row without values is that of a row of zeros
+    x, w = torch.empty(300, 0, dtype=BF16, device="cuda"), torch.empty(0, dtype=BF16, device="cuda")
+    for call in (lambda: fp8bq.rmsnorm_quant_i8(x, w), lambda: fp8bq.rmsnorm_quant_i8(x, w, x),
+                 lambda: fp8bq.quant_act_i8(x), lambda: fp8bq.quant_weight_i8(x.float())):
+        used = torch.full((300,), 7.0, device="cuda")  # memory that the next tensor of this size may get
+        del used
+        codes, scales = call()[:2]
+        assert codes.shape == (300, 0) and scales.shape == (300,) and bool((scales == 1).all())
