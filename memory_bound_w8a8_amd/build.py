@@ -5,8 +5,9 @@
 Each .hip source under csrc/ is compiled to an object in _build/ (in
 parallel), then linked into memory_bound_w8a8_amd/libfp8bq.so. Beside it the
 Python module _binding.so is built from binding.cpp (host code only, against
-the installed torch) and linked to that library. The compile always runs (no
-up-to-date check) so that a stale library is never shipped.
+the installed torch) and linked to that library; where that fails, the error
+is raised with libfp8bq.so in place, which needs hipcc alone. The compile always
+runs (no up-to-date check) so that a stale library is never shipped.
 """
 
 import concurrent.futures
@@ -81,6 +82,10 @@ def _binding_link(obj, out):
 
 
 def build(verbose: bool = False) -> str:
+    def say(out):
+        if verbose and out.strip():
+            print(out)
+
     hipcc = _hipcc()
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(f for f in os.listdir(CSRC) if f.endswith(".hip"))
@@ -88,20 +93,23 @@ def build(verbose: bool = False) -> str:
     form = lambda s: [] if s in ACC_FORM_SOURCES else VGPR_FORM  # noqa: E731
     cmds = [[hipcc, *HIPCC_FLAGS, *form(s), "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(sources, objs)]
     binding_obj = os.path.join(BUILD, "binding.o")
-    cmds.append(_binding_compile(binding_obj))
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(cmds))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(cmds) + 1)) as ex:
+        binding = ex.submit(lambda: _run(_binding_compile(binding_obj)))
         for out in ex.map(_run, cmds):
-            if verbose and out.strip():
-                print(out)
+            say(out)
     tmp = LIB + ".tmp"
-    out = _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp])
-    if verbose and out.strip():
-        print(out)
+    say(_run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]))
     os.replace(tmp, LIB)
-    tmp = BINDING + ".tmp"
-    out = _run(_binding_link(binding_obj, tmp))
-    if verbose and out.strip():
-        print(out)
+    # The library is there; the module needs more (g++, torch's headers). One of
+    # an earlier build does not outlive a failure.
+    try:
+        say(binding.result())
+        tmp = BINDING + ".tmp"
+        say(_run(_binding_link(binding_obj, tmp)))
+    except Exception:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        raise
     os.replace(tmp, BINDING)
     return LIB
 
