@@ -1,5 +1,7 @@
 """GPU: the step's operators at the limits their headers state."""
 
+import sys
+
 import pytest
 import torch
 
@@ -83,3 +85,19 @@ def test_depth_zero_gives_scales_of_one(way):
         del used
         codes, scales = call()[:2]
         assert codes.shape == (300, 0) and scales.shape == (300,) and bool((scales == 1).all())
+
+
+def test_without_the_native_binding(monkeypatch):
+    x, w = torch.randn(5, 256, device="cuda").to(BF16), torch.ones(256, dtype=BF16, device="cuda")
+    a, s = torch.ones(4, 128, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    p, d = torch.full((2, 2, 8), 0.125, device="cuda"), torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    u = torch.full((2, 1), 0.5, device="cuda")
+    calls = (lambda: fp8bq.rmsnorm_quant(x, w, x), lambda: fp8bq.rmsnorm_quant_i8(x, w),
+             lambda: (fp8bq.gemm_i8(a, s, a, s),), lambda: fp8bq.verify_drafts(p, d, u, u[:, 0].contiguous()))
+    want = [call() for call in calls]
+    monkeypatch.setattr(step, "_direct", None)
+    monkeypatch.setitem(sys.modules, "memory_bound_w8a8_amd._binding", None)
+    monkeypatch.delattr(fp8bq, "_binding", raising=False)
+    with pytest.warns(RuntimeWarning, match="_binding.so is missing"):
+        got = [call() for call in calls]
+    assert all(torch.equal(a_, b_) for one, other in zip(got, want) for a_, b_ in zip(one, other))
