@@ -37,9 +37,10 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // sums are in accumulation registers that stay where they are: from the
 // builtin the compiler renames the sums of a loop and moves them back (4 moves
 // per MFMA in a 128 x 128 wave tile). The compiler sees no MFMA here, so the
-// distances it would keep are kept by the callers: 4 or more other MFMAs
-// between two on the same sums, and mfma_settle() before the first (the sums
-// just written) and after the last (before they are read). A kernel that keeps
+// distances it would keep are kept by the callers: mfma_settle() before the
+// first (the sums just written) and after the last (before they are read). Two
+// on the same sums need none: source and destination are the same registers,
+// and the compiler too lets such a pair follow directly. A kernel that keeps
 // sums and spilled values in these registers would move them between: every
 // instance has exactly its sums there.
 __device__ __forceinline__ void mfma_acc_16x16x64_i8(const v4u& a, const v4u& b, v4i& c) {
@@ -115,7 +116,7 @@ struct I8Tile {
   static constexpr bool kAhead = kWaves == 4 && kI * kJ <= 12;
   static_assert((BM + BN) / 8 % kWaves == 0, "every wave issues the same number of copies");
   static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM % 8 == 0, "16-row fragments");
-  static_assert(kI * kJ >= 4, "MFMAs between two on the same sums");
+  static_assert(kI * kJ >= 4, "other MFMAs while one's sums are under way: for speed, not needed for the result");
   static_assert(STAGES >= 2, "the stage being filled is not the one being read");
 };
 
@@ -147,6 +148,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tiled_kernel(int64_t m_r
   __shared__ float lds_sa[BM], lds_sw[BN];
   __shared__ __attribute__((aligned(16))) unsigned char lds_unread[FETCH ? 256 * WAVES : 1];
   static_assert(!FETCH || (BM == 64 * WAVES && BN == 64 * WAVES), "a line of the tile per thread");
+  // the first step's wait allows one fetch besides the copies of the stages after
+  // the next: with more stages than two it would allow a copy too many
+  static_assert(!FETCH || STAGES == 2, "the wait of a step with fetches is counted for two stages");
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
