@@ -55,9 +55,12 @@ PyObject* pair_of(PyObject* a, PyObject* b) {
 // step.py.
 template <typename F>
 PyObject* guarded(F f) {
-  HANDLE_TH_ERRORS
-  return f();
-  END_HANDLE_TH_ERRORS
+  try {
+    return f();
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
+    return nullptr;
+  }
 }
 
 // The device and the stream a call ends with.
